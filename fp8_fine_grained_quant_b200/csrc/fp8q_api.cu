@@ -14,8 +14,10 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "fp8q.h"
+#include "fp8q_ckpt.cuh"
 #include "fp8q_gemm.cuh"
 #include "fp8q_gemm_mx.cuh"
+#include "fp8q_moe.cuh"
 #include "fp8q_ptx.cuh"
 #include "fp8q_quant.cuh"
 
@@ -769,6 +771,245 @@ int fp8_gemm_wgrad(const uint8_t* q_dy_t, const float* s_dy, const uint8_t* q_x_
   // C [N, K] = A [N, Mp] * B [K, Mp]^T: GEMM rows N, columns K, depth Mp
   GemmCall g{q_dy_t, s_dy, q_x_t, s_x, dw_bf16, nullptr, nullptr, N, N, K, Mp, 1, N / kBlockM, 0, 1};
   return launch_gemm<kTileN, kStages128, Sched::kDense, true, true, true>(g, *dev, stream);
+}
+
+// ---------------------------------------------------------------- mixture of experts
+// Sizes shared by the routing, layout, dispatch and combine entry points: a
+// token's experts are one lane of a warp each, and the kernels number tokens'
+// tiles in 32 bits.
+static bool bad_topk(int64_t T, int64_t top_k) { return T < 0 || T >= kMaxRows || top_k < 1 || top_k > kMaxTopK; }
+static bool bad_tokens(int64_t T, int64_t top_k, int64_t D, int64_t rows) {
+  return bad_topk(T, top_k) || D < 0 || D % 128 || D >= kMaxRows || rows < 0 || rows >= kMaxRows ||
+         T * (D / 128) >= kMaxRows;
+}
+// The contiguous layout's arrays: both or neither, over whole 128-row blocks.
+static int check_layout(const int32_t* m_indices, const int32_t* counts, int64_t E, int64_t rows) {
+  if (!m_indices && !counts) return FP8Q_OK;
+  if (E < 1 || E > kMaxExperts || rows % 128) return FP8Q_ERR_SHAPE;
+  if (!m_indices || !counts) return FP8Q_ERR_NULL;
+  if (!aligned(m_indices, 4) || !aligned(counts, 4)) return FP8Q_ERR_ALIGN;
+  return FP8Q_OK;
+}
+static int launched() {
+  if (cudaGetLastError() != cudaSuccess) return FP8Q_ERR_CUDA;
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return FP8Q_OK;
+}
+
+int fp8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t E, const float* bias, int sigmoid,
+                  int64_t top_k, int64_t n_group, int64_t topk_group, int64_t group_top, int renorm, float scale,
+                  int32_t* ids, float* weights, cudaStream_t stream) {
+  FP8Q_API_RANGE();
+  if (bad_topk(T, top_k) || E < 1 || E > kMaxExperts || n_group < 1 || n_group > kMaxGroups || E % n_group ||
+      topk_group < 1 || topk_group > n_group || group_top < 1 || group_top > 2 ||
+      top_k > topk_group * (E / n_group))
+    return FP8Q_ERR_SHAPE;
+  if (T == 0) return FP8Q_OK;
+  if (!logits || !ids || !weights) return FP8Q_ERR_NULL;
+  if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return FP8Q_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc) return rc;
+  RouteArgs a{logits, bias, ids, weights, T, static_cast<int32_t>(E), static_cast<int32_t>(top_k),
+              static_cast<int32_t>(n_group), static_cast<int32_t>(topk_group), static_cast<int32_t>(group_top),
+              sigmoid != 0, renorm != 0, scale};
+  const unsigned grid = static_cast<unsigned>((T + kRouteWarps - 1) / kRouteWarps);
+  const size_t smem = static_cast<size_t>(kRouteWarps) * E * sizeof(double);
+  if (logits_bf16)
+    moe_route_kernel<true><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
+  else
+    moe_route_kernel<false><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
+  return launched();
+}
+
+int fp8_moe_route_bwd(const void* logits, int logits_bf16, int64_t T, int64_t E, const int32_t* ids,
+                      const float* dweights, int sigmoid, int64_t top_k, int renorm, float scale, void* dlogits,
+                      cudaStream_t stream) {
+  FP8Q_API_RANGE();
+  if (bad_topk(T, top_k) || E < 1 || E > kMaxExperts) return FP8Q_ERR_SHAPE;
+  if (T == 0) return FP8Q_OK;
+  if (!logits || !ids || !dweights || !dlogits) return FP8Q_ERR_NULL;
+  const uintptr_t la = logits_bf16 ? 2 : 4;
+  if (!aligned(logits, la) || !aligned(dlogits, la) || !aligned(ids, 4) || !aligned(dweights, 4))
+    return FP8Q_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc) return rc;
+  RouteBwdArgs a{logits, ids, dweights, dlogits, T, static_cast<int32_t>(E), static_cast<int32_t>(top_k),
+                 sigmoid != 0, renorm != 0, scale};
+  const unsigned grid = static_cast<unsigned>((T + kRouteWarps - 1) / kRouteWarps);
+  const size_t smem = static_cast<size_t>(kRouteWarps) * E * sizeof(float);
+  if (logits_bf16)
+    moe_route_bwd_kernel<true><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
+  else
+    moe_route_bwd_kernel<false><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
+  return launched();
+}
+
+static int run_layout(const LayoutArgs& a, cudaStream_t stream) {
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc) return rc;
+  const int64_t ctas = (a.n + kLayoutThreads - 1) / kLayoutThreads;
+  moe_layout_kernel<<<static_cast<unsigned>(ctas ? ctas : 1), kLayoutThreads, 0, stream>>>(a);
+  return launched();
+}
+
+int fp8_moe_layout_contiguous(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* slots,
+                              int32_t* m_indices, int32_t* counts, cudaStream_t stream) {
+  FP8Q_API_RANGE();
+  if (bad_topk(T, top_k) || E < 1 || E > kMaxExperts) return FP8Q_ERR_SHAPE;
+  const int64_t n = T * top_k;
+  const int64_t blocks = (n + 127 * (n < E ? n : E)) / 128;
+  if (blocks * 128 >= kMaxRows) return FP8Q_ERR_SHAPE;
+  if (!counts || (n && (!ids || !slots || !m_indices))) return FP8Q_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(slots, 4) || !aligned(m_indices, 4) || !aligned(counts, 4)) return FP8Q_ERR_ALIGN;
+  return run_layout(LayoutArgs{ids, n, static_cast<int32_t>(E), 0, slots, m_indices, blocks, counts}, stream);
+}
+
+int fp8_moe_layout_masked(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int64_t cap, int32_t* slots,
+                          int32_t* masked_m, cudaStream_t stream) {
+  FP8Q_API_RANGE();
+  if (bad_topk(T, top_k) || E < 1 || E > kMaxExperts || cap < 128 || cap % 128 || cap >= kMaxRows ||
+      E * cap >= kMaxRows || T * top_k >= kMaxRows)
+    return FP8Q_ERR_SHAPE;
+  const int64_t n = T * top_k;
+  if (!masked_m || (n && (!ids || !slots))) return FP8Q_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(slots, 4) || !aligned(masked_m, 4)) return FP8Q_ERR_ALIGN;
+  return run_layout(LayoutArgs{ids, n, static_cast<int32_t>(E), cap, slots, nullptr, 0, masked_m}, stream);
+}
+
+int fp8_moe_dispatch_1x128(const void* x_bf16, int64_t T, int64_t D, const int32_t* slots, int64_t top_k, int64_t rows,
+                           const int32_t* m_indices, const int32_t* counts, int64_t E, uint8_t* q, float* s,
+                           cudaStream_t stream) {
+  FP8Q_API_RANGE();
+  if (bad_tokens(T, top_k, D, rows)) return FP8Q_ERR_SHAPE;
+  int rc = check_layout(m_indices, counts, E, rows);
+  if (rc) return rc;
+  if (T == 0 || D == 0 || rows == 0) return FP8Q_OK;
+  if (!x_bf16 || !slots || !q || !s) return FP8Q_ERR_NULL;
+  if (!aligned(x_bf16, 32) || !aligned(slots, 4) || !aligned(q, 16) || !aligned(s, 4)) return FP8Q_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  rc = device_info(&dev);
+  if (rc) return rc;
+  DispatchArgs a{static_cast<const uint8_t*>(x_bf16), slots, static_cast<int32_t>(top_k),
+                 static_cast<int32_t>(D / 128), T * (D / 128), rows, m_indices, counts, static_cast<int32_t>(E), q, s};
+  int64_t grid = (a.num_tiles + 31) / 32;  // 32 tiles per CTA pass
+  if (m_indices && grid < rows / 8) grid = rows / 8;  // a warp per row of padding
+  const int64_t cap = static_cast<int64_t>(dev->num_sms) * 10;
+  if (grid > cap) grid = cap;
+  moe_dispatch_1x128_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(a);
+  return launched();
+}
+
+int fp8_moe_combine(const void* y_bf16, int64_t rows, int64_t D, const int32_t* slots, const float* weights, int64_t T,
+                    int64_t top_k, void* out_bf16, cudaStream_t stream) {
+  FP8Q_API_RANGE();
+  if (bad_tokens(T, top_k, D, rows)) return FP8Q_ERR_SHAPE;
+  if (T == 0 || D == 0) return FP8Q_OK;
+  if ((!y_bf16 && rows) || !slots || !out_bf16) return FP8Q_ERR_NULL;
+  if (!aligned(y_bf16, 16) || !aligned(slots, 4) || !aligned(weights, 4) || !aligned(out_bf16, 16))
+    return FP8Q_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc) return rc;
+  CombineArgs a{static_cast<const uint8_t*>(y_bf16), slots, weights, static_cast<uint8_t*>(out_bf16),
+                static_cast<int32_t>(top_k), static_cast<int32_t>(D / 128), T * (D / 128), rows};
+  int64_t grid = (a.num_tiles + 15) / 16;  // 16 tiles per CTA pass
+  const int64_t cap = static_cast<int64_t>(dev->num_sms) * 16;
+  if (grid > cap) grid = cap;
+  moe_combine_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(a);
+  return launched();
+}
+
+int fp8_moe_combine_bwd(const void* dout_bf16, const void* y_bf16, int64_t rows, int64_t D, const int32_t* slots,
+                        const float* weights, int64_t T, int64_t top_k, const int32_t* m_indices,
+                        const int32_t* counts, int64_t E, void* dy_bf16, float* dweights, cudaStream_t stream) {
+  FP8Q_API_RANGE();
+  if (bad_tokens(T, top_k, D, rows)) return FP8Q_ERR_SHAPE;
+  int rc = check_layout(m_indices, counts, E, rows);
+  if (rc) return rc;
+  if (T == 0 || D == 0) return FP8Q_OK;
+  if (!dout_bf16 || (rows && (!y_bf16 || !dy_bf16)) || !slots || !weights || !dweights) return FP8Q_ERR_NULL;
+  if (!aligned(dout_bf16, 16) || !aligned(y_bf16, 16) || !aligned(dy_bf16, 16) || !aligned(slots, 4) ||
+      !aligned(weights, 4) || !aligned(dweights, 4))
+    return FP8Q_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  rc = device_info(&dev);
+  if (rc) return rc;
+  CombineBwdArgs a{static_cast<const uint8_t*>(dout_bf16), static_cast<const uint8_t*>(y_bf16), slots, weights,
+                   static_cast<uint8_t*>(dy_bf16), dweights, static_cast<int32_t>(top_k), T, D, rows, m_indices,
+                   counts, static_cast<int32_t>(E)};
+  int64_t grid = T;
+  if (m_indices && grid < rows / 8) grid = rows / 8;  // a warp per row of padding
+  const int64_t cap = static_cast<int64_t>(dev->num_sms) * 16;
+  if (grid > cap) grid = cap;
+  moe_combine_bwd_kernel<<<static_cast<unsigned>(grid), kCombineBwdThreads, 0, stream>>>(a);
+  return launched();
+}
+
+// ---------------------------------------------------------------- 8-bit checkpoints
+int fp8_swiglu_ckpt_1x128(const void* c1_bf16, int64_t rows, int64_t inter, uint8_t* qh, float* sh, uint8_t* qc,
+                          float* sc, cudaStream_t stream) {
+  FP8Q_API_RANGE();
+  if (rows < 0 || inter < 0 || inter % 128 || rows >= kMaxRows || inter >= kMaxRows / 2 ||
+      rows * (inter / 128) >= kMaxRows)
+    return FP8Q_ERR_SHAPE;
+  if (rows == 0 || inter == 0) return FP8Q_OK;
+  if (!c1_bf16 || !qh || !sh || !qc || !sc) return FP8Q_ERR_NULL;
+  if (!aligned(c1_bf16, 32) || !aligned(qh, 16) || !aligned(sh, 4) || !aligned(qc, 16) || !aligned(sc, 4))
+    return FP8Q_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc) return rc;
+  const int64_t tiles = rows * (inter / 128);
+  int64_t grid = (tiles + 31) / 32;  // 32 tiles per CTA pass
+  const int64_t cap = static_cast<int64_t>(dev->num_sms) * 8;
+  if (grid > cap) grid = cap;
+  swiglu_ckpt_1x128_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(static_cast<const uint8_t*>(c1_bf16), qh,
+                                                                          sh, qc, sc, inter, tiles);
+  return launched();
+}
+
+int fp8_swiglu_bwd_1x128(const void* dh_bf16, const uint8_t* qc, const float* sc, int64_t rows, int64_t inter,
+                         void* dc_bf16, uint8_t* q, float* s, cudaStream_t stream) {
+  FP8Q_API_RANGE();
+  if (rows < 0 || inter < 0 || inter % 128 || rows >= kMaxRows || inter >= kMaxRows / 2 ||
+      rows * (inter / 128) >= kMaxRows)
+    return FP8Q_ERR_SHAPE;
+  if (rows == 0 || inter == 0) return FP8Q_OK;
+  if (!dh_bf16 || !qc || !sc || !dc_bf16 || !q || !s) return FP8Q_ERR_NULL;
+  if (!aligned(dh_bf16, 32) || !aligned(qc, 16) || !aligned(sc, 4) || !aligned(dc_bf16, 16) || !aligned(q, 16) ||
+      !aligned(s, 4))
+    return FP8Q_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc) return rc;
+  const int64_t tiles = rows * (inter / 128);
+  int64_t grid = (tiles + 31) / 32;  // 32 tiles per CTA pass
+  const int64_t cap = static_cast<int64_t>(dev->num_sms) * 8;
+  if (grid > cap) grid = cap;
+  swiglu_bwd_1x128_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(
+      static_cast<const uint8_t*>(dh_bf16), qc, sc, static_cast<uint8_t*>(dc_bf16), q, s, inter, tiles);
+  return launched();
+}
+
+int fp8_ckpt_128x1_t(const uint8_t* q, const float* s, int64_t M, int64_t K, int64_t Mp, uint8_t* qt, float* st,
+                     cudaStream_t stream) {
+  FP8Q_API_RANGE();
+  if (M < 0 || K < 0 || K % 128 || Mp < M || Mp % 128 || Mp >= kMaxRows || K >= kMaxRows) return FP8Q_ERR_SHAPE;
+  if (Mp == 0 || K == 0) return FP8Q_OK;
+  if ((M && (!q || !s)) || !qt || !st) return FP8Q_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(s, 4) || !aligned(qt, 16) || !aligned(st, 16)) return FP8Q_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  int rc = device_info(&dev);
+  if (rc) return rc;
+  const int64_t blocks = (Mp / 128) * (K / 128);
+  const int64_t cap = static_cast<int64_t>(dev->num_sms) * 24;
+  const int64_t grid = blocks < cap ? blocks : cap;
+  ckpt_128x1_t_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(q, s, qt, st, M, K, Mp, blocks);
+  return launched();
 }
 
 const char* fp8q_status_string(int status) {

@@ -1,0 +1,658 @@
+// fp8q_moe.cuh -- what surrounds the grouped GEMMs in a mixture-of-experts
+// layer: the choice of experts from router logits and its gradient, the row
+// layouts of the grouped GEMMs, the tokens quantized into them, and the
+// weighted sum of the experts' outputs and its gradient.
+//
+// The pages name the two grouped layouts ("Deepgemm lancado no dia 4 da semana
+// de codigo aberto Deepseek", "Principais caracteristicas") and the 1x128
+// activation tiles ("The Insider Secrets Of Deepseek Discovered", Figure 7
+// (a)); these kernels produce and consume those layouts.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cfloat>
+#include <cmath>
+#include <cstdint>
+
+#include "fp8q_ptx.cuh"
+#include "fp8q_quant.cuh"
+
+namespace fp8q {
+
+constexpr int kMaxExperts = 1024;  // experts of a router or layout
+constexpr int kMaxTopK = 32;       // experts of one token (one lane of a warp each)
+constexpr int kMaxGroups = 32;     // expert groups (one lane each)
+
+__device__ __forceinline__ double neg_inf_f64() { return __longlong_as_double(0xFFF0000000000000ll); }
+__device__ __forceinline__ float neg_inf_f32() { return __int_as_float(0xFF800000); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// Expert choice.  For each token with logits l over E experts:
+//   score   p_e = softmax(l)_e or 1 / (1 + exp(-l_e));
+//   key     p_e + bias_e with a bias, else p_e (the order of l_e itself);
+//   groups  the E / n_group experts of a group share the sum of the group's
+//           best one or two keys; the topk_group best groups stay;
+//   choice  the top_k best keys of the experts that stay, best first;
+//   weights scale * p_e, or scale * p_e / sum of the chosen p (renorm): the
+//           bias moves the choice, not the weights.
+// Equal keys (and groups) go to the lower index.  An expert whose logit or
+// bias is -inf or NaN is never chosen; places that find no expert get id -1
+// and weight 0.  A logit of +inf counts as the largest finite FP32.
+//
+// Two keys that differ by less than their FP32 error would make the choice
+// depend on how the scores were evaluated, so keys are compared in binary64.
+//
+// One warp per token; the keys of its row lie in shared memory.
+// ---------------------------------------------------------------------------
+struct RouteArgs {
+  const void* logits;  // [T, E] f32 or bf16
+  const float* bias;   // [E] or null
+  int32_t* ids;        // [T, top_k]
+  float* weights;      // [T, top_k]
+  int64_t T;
+  int32_t E, top_k, n_group, topk_group, group_top;
+  int32_t sigmoid, renorm;
+  float scale;
+};
+
+// Logit e of a row as FP32; -inf for NaN, the largest finite value for +inf.
+template <bool kBf16>
+__device__ __forceinline__ float load_logit(const void* row, int e) {
+  float l;
+  if constexpr (kBf16)
+    l = __bfloat162float(static_cast<const __nv_bfloat16*>(row)[e]);
+  else
+    l = static_cast<const float*>(row)[e];
+  if (!(l > neg_inf_f32())) return neg_inf_f32();
+  return fminf(l, FLT_MAX);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ const void* logits_row(const void* logits, int64_t t, int E) {
+  return static_cast<const uint8_t*>(logits) + t * E * (kBf16 ? 2 : 4);
+}
+
+// Weights of the chosen experts: lane j holds id (or -1) and returns its weight.
+// Sigmoid ratios are formed from e^(l - m) / (1 + e^l) with m = min(0, largest
+// chosen logit), which stays finite and nonzero when every chosen score
+// underflows.  row_max and row_sum are the softmax statistics of the whole row
+// (used without renorm).
+__device__ __forceinline__ float route_weight(float l, bool found, bool sigmoid, bool renorm, float scale,
+                                              float row_max, float row_sum) {
+  float p;
+  if (renorm) {
+    const float m = warp_max(found ? l : neg_inf_f32());
+    if (sigmoid) {
+      const float c = fminf(m, 0.0f);
+      p = l > 0.0f ? 1.0f / (1.0f + expf(-l)) : expf(l - c) / (1.0f + expf(l));
+    } else {
+      p = expf(l - m);
+    }
+    const float total = warp_sum(found ? p : 0.0f);
+    p /= total;
+  } else {
+    p = sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - row_max) / row_sum;
+  }
+  return found ? scale * p : 0.0f;
+}
+
+// The choice in binary64.  keys: the warp's E doubles of shared memory.
+// Returns the id of place `lane` (or -1).
+template <bool kBf16>
+__device__ __noinline__ int route_choose_f64(const RouteArgs& a, const void* row, double* keys, float row_max) {
+  const int lane = threadIdx.x & 31;
+  const int E = a.E;
+  double sum = 0.0;
+  if (!a.sigmoid) {
+    for (int e = lane; e < E; e += 32) {
+      const float l = load_logit<kBf16>(row, e);
+      if (l > neg_inf_f32()) sum += exp(static_cast<double>(l) - static_cast<double>(row_max));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+  }
+  const bool by_score = a.bias != nullptr || a.n_group > 1;
+  for (int e = lane; e < E; e += 32) {
+    const float l = load_logit<kBf16>(row, e);
+    double k = static_cast<double>(l);
+    if (l > neg_inf_f32() && by_score) {
+      k = a.sigmoid ? 1.0 / (1.0 + exp(-k)) : exp(k - static_cast<double>(row_max)) / sum;
+      if (a.bias != nullptr) {
+        k += static_cast<double>(a.bias[e]);
+        if (!(k > neg_inf_f64())) k = neg_inf_f64();
+      }
+    }
+    keys[e] = k;
+  }
+  __syncwarp();
+  if (a.n_group > 1) {
+    const int size = E / a.n_group;
+    double total = neg_inf_f64();
+    if (lane < a.n_group) {
+      double b1 = neg_inf_f64(), b2 = neg_inf_f64();
+      for (int i = 0; i < size; ++i) {
+        const double k = keys[lane * size + i];
+        b2 = fmax(b2, fmin(b1, k));
+        b1 = fmax(b1, k);
+      }
+      total = a.group_top == 2 && b2 > neg_inf_f64() ? b1 + b2 : b1;
+    }
+    int ahead = 0;
+    for (int h = 0; h < a.n_group; ++h) {
+      const double o = __shfl_sync(0xFFFFFFFFu, total, h);
+      ahead += o > total || (o == total && h < lane);
+    }
+    const uint32_t keep = __ballot_sync(0xFFFFFFFFu, lane < a.n_group && ahead < a.topk_group);
+    __syncwarp();
+    for (int e = lane; e < E; e += 32) {
+      if (!((keep >> (e / size)) & 1u))
+        keys[e] = neg_inf_f64();
+      else if (a.bias == nullptr)
+        keys[e] = static_cast<double>(load_logit<kBf16>(row, e));
+    }
+    __syncwarp();
+  }
+  int mine = -1;
+  for (int j = 0; j < a.top_k; ++j) {
+    double best = neg_inf_f64();
+    int at = E;
+    for (int e = lane; e < E; e += 32) {
+      if (keys[e] > best) {
+        best = keys[e];
+        at = e;
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const double o = __shfl_xor_sync(0xFFFFFFFFu, best, off);
+      const int oa = __shfl_xor_sync(0xFFFFFFFFu, at, off);
+      if (o > best || (o == best && oa < at)) {
+        best = o;
+        at = oa;
+      }
+    }
+    if (!(best > neg_inf_f64())) break;  // uniform: every lane holds the same best
+    if (lane == j) mine = at;
+    if (lane == (at & 31)) keys[at] = neg_inf_f64();  // the lane that scans `at`
+    __syncwarp();
+  }
+  return mine;
+}
+
+constexpr int kRouteWarps = 4;
+
+template <bool kBf16>
+__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(RouteArgs a) {
+  extern __shared__ double route_keys[];  // [kRouteWarps][E]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
+  if (t >= a.T) return;
+  const void* row = logits_row<kBf16>(a.logits, t, a.E);
+  float row_max = neg_inf_f32(), row_sum = 0.0f;
+  if (!a.sigmoid) {
+    for (int e = lane; e < a.E; e += 32) row_max = fmaxf(row_max, load_logit<kBf16>(row, e));
+    row_max = warp_max(row_max);
+    for (int e = lane; e < a.E; e += 32) {
+      const float l = load_logit<kBf16>(row, e);
+      if (l > neg_inf_f32()) row_sum += expf(l - row_max);
+    }
+    row_sum = warp_sum(row_sum);
+  }
+  const int id = route_choose_f64<kBf16>(a, row, route_keys + static_cast<int64_t>(warp) * a.E, row_max);
+  const float l = id >= 0 ? load_logit<kBf16>(row, id) : 0.0f;
+  const float w = route_weight(l, id >= 0, a.sigmoid, a.renorm, a.scale, row_max, row_sum);
+  if (lane < a.top_k) {
+    a.ids[t * a.top_k + lane] = id;
+    a.weights[t * a.top_k + lane] = w;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the weights with respect to the logits (the choice itself is
+// constant).  With g the gradient of the weights, over the chosen j:
+//   softmax, renorm:  r = softmax over the chosen;  dl_j = scale r_j (g_j - <g, r>)
+//   sigmoid, renorm:  r = p / sum p;                dl_j = scale r_j (g_j - <g, r>) (1 - p_j)
+//   sigmoid:          dl_j = scale g_j p_j (1 - p_j)
+//   softmax:          dl_e = scale p_e (d_e - <g, p>), d_e = the g of e, 0 where e was not chosen
+// Every other logit gets 0.  Places with an id outside [0, E) count for
+// nothing; an id that appears twice gets the sum.  1 - p_j is evaluated as
+// 1 / (1 + exp(l_j)), which keeps its digits when p_j is close to 1.
+//
+// One warp per token; the row of gradients is gathered in shared memory.
+// ---------------------------------------------------------------------------
+struct RouteBwdArgs {
+  const void* logits;
+  const int32_t* ids;
+  const float* dweights;
+  void* dlogits;
+  int64_t T;
+  int32_t E, top_k, sigmoid, renorm;
+  float scale;
+};
+
+template <bool kBf16>
+__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_bwd_kernel(RouteBwdArgs a) {
+  extern __shared__ float route_grad[];  // [kRouteWarps][E]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
+  if (t >= a.T) return;
+  const int E = a.E;
+  const void* row = logits_row<kBf16>(a.logits, t, E);
+  float* d = route_grad + static_cast<int64_t>(warp) * E;
+  for (int e = lane; e < E; e += 32) d[e] = 0.0f;
+  int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
+  if (id >= E) id = -1;
+  float g = 0.0f, l = neg_inf_f32();
+  if (id >= 0) {
+    g = a.dweights[t * a.top_k + lane];
+    l = load_logit<kBf16>(row, id);
+  }
+  const bool has = id >= 0 && l > neg_inf_f32();
+  const bool dense = !a.sigmoid && !a.renorm;
+  float v = g;  // dense: the gradient of p; else of the logit
+  if (!dense) {
+    const float not_p = a.sigmoid ? 1.0f / (1.0f + expf(l)) : 1.0f;
+    if (a.renorm) {
+      const float r = route_weight(l, has, a.sigmoid, true, 1.0f, 0.0f, 1.0f);
+      const float mean = warp_sum(has ? g * r : 0.0f);
+      v = a.scale * r * (g - mean) * not_p;
+    } else {
+      v = a.scale * g * (1.0f / (1.0f + expf(-l))) * not_p;
+    }
+  }
+  if (!has) v = 0.0f;
+  // an id that appears more than once: the sum, in place order
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, has ? id : -1 - lane);
+  if (__any_sync(0xFFFFFFFFu, __popc(same) > 1)) {
+    float total = 0.0f;
+    for (int j = 0; j < a.top_k; ++j) {
+      const float o = __shfl_sync(0xFFFFFFFFu, v, j);
+      if ((same >> j) & 1u) total += o;
+    }
+    v = total;
+  }
+  __syncwarp();
+  if (has) d[id] = v;
+  __syncwarp();
+  float row_max = neg_inf_f32(), inv_sum = 0.0f, mean = 0.0f;
+  if (dense) {
+    float sum = 0.0f, dot = 0.0f;
+    for (int e = lane; e < E; e += 32) row_max = fmaxf(row_max, load_logit<kBf16>(row, e));
+    row_max = warp_max(row_max);
+    for (int e = lane; e < E; e += 32) {
+      const float x = load_logit<kBf16>(row, e);
+      const float p = x > neg_inf_f32() ? expf(x - row_max) : 0.0f;
+      sum += p;
+      dot += p * d[e];
+    }
+    sum = warp_sum(sum);
+    dot = warp_sum(dot);
+    inv_sum = sum > 0.0f ? 1.0f / sum : 0.0f;
+    mean = dot * inv_sum;
+  }
+  for (int e = lane; e < E; e += 32) {
+    float o = d[e];
+    if (dense) {
+      const float x = load_logit<kBf16>(row, e);
+      o = x > neg_inf_f32() ? a.scale * (expf(x - row_max) * inv_sum) * (o - mean) : 0.0f;
+    }
+    if constexpr (kBf16)
+      static_cast<__nv_bfloat16*>(a.dlogits)[t * E + e] = __float2bfloat16_rn(o);
+    else
+      static_cast<float*>(a.dlogits)[t * E + e] = o;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Row layouts of the grouped GEMMs from the chosen experts.  Entry i = t *
+// top_k + j of ids goes to the row
+//   contiguous:  128 * (whole blocks of the experts before) + rank,
+//   masked:      expert * cap + rank (no row, -1, once the rank reaches cap),
+// rank being the number of earlier entries with the same expert, so the layout
+// does not depend on any order of execution.  Ids outside [0, E) get no row.
+//
+// One CTA per 1024 entries.  Each counts the experts of all entries, those
+// before its own apart (integer shared-memory atomics: their order does not
+// change a count), then ranks its own: __match_any within a warp, a byte
+// table [warp][expert] across warps.  One launch and no workspace, at the
+// price of every CTA reading all ids.
+// ---------------------------------------------------------------------------
+struct LayoutArgs {
+  const int32_t* ids;
+  int64_t n;          // entries
+  int32_t E;
+  int64_t cap;        // masked: rows of an expert; 0: contiguous
+  int32_t* slots;     // [n]
+  int32_t* m_indices; // contiguous: [blocks]
+  int64_t blocks;
+  int32_t* counts;    // contiguous: entries of each expert; masked: min(entries, cap)
+};
+
+constexpr int kLayoutThreads = 1024;
+
+__global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(LayoutArgs a) {
+  __shared__ int32_t before[kMaxExperts];  // entries of each expert ahead of this CTA's
+  __shared__ int32_t all[kMaxExperts];     // the others; then all entries
+  __shared__ int32_t start[kMaxExperts + 1];
+  __shared__ uint8_t in_warp[32][kMaxExperts];
+  __shared__ int32_t warp_total[32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int E = a.E;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kLayoutThreads;
+  before[tid] = 0;
+  all[tid] = 0;
+  for (int e = tid; e < 32 * kMaxExperts / 4; e += kLayoutThreads) reinterpret_cast<uint32_t*>(in_warp)[e] = 0u;
+  __syncthreads();
+  for (int64_t i = tid; i < a.n; i += kLayoutThreads) {
+    const int e = a.ids[i];
+    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E)) atomicAdd(i < first ? &before[e] : &all[e], 1);
+  }
+  const int64_t mine = first + tid;
+  int e = mine < a.n ? a.ids[mine] : -1;
+  if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(E)) e = -1;
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+  int rank = __popc(same & ((1u << lane) - 1u));
+  if (e >= 0 && rank == 0) in_warp[warp][e] = static_cast<uint8_t>(__popc(same));
+  __syncthreads();
+  // whole entries of expert tid, and the exclusive prefix of the experts' rows
+  const int count = tid < E ? before[tid] + all[tid] : 0;
+  const int size = (count + 127) >> 7;  // blocks of 128 rows
+  int incl = size;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+    if (lane >= off) incl += o;
+  }
+  if (lane == 31) warp_total[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const int own = warp_total[lane];
+    int s = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, s, off);
+      if (lane >= off) s += o;
+    }
+    warp_total[lane] = s - own;
+  }
+  __syncthreads();
+  start[tid] = warp_total[warp] + incl - size;
+  if (tid == kLayoutThreads - 1) start[kMaxExperts] = warp_total[warp] + incl;
+  __syncthreads();
+  if (mine < a.n) {
+    int64_t slot = -1;
+    if (e >= 0) {
+      for (int w = 0; w < warp; ++w) rank += in_warp[w][e];
+      const int64_t r = static_cast<int64_t>(before[e]) + rank;
+      if (a.cap > 0)
+        slot = r < a.cap ? e * a.cap + r : -1;
+      else
+        slot = static_cast<int64_t>(start[e]) * 128 + r;
+    }
+    a.slots[mine] = static_cast<int32_t>(slot);
+  }
+  if (blockIdx.x == 0 && tid < E)
+    a.counts[tid] = a.cap > 0 && count > a.cap ? static_cast<int32_t>(a.cap) : count;
+  if (a.cap == 0) {
+    // the expert of each block: the last whose first block is not past it and that has blocks
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kLayoutThreads;
+    for (int64_t b = static_cast<int64_t>(blockIdx.x) * kLayoutThreads + tid; b < a.blocks; b += stride) {
+      int owner = -1;
+      if (b < start[kMaxExperts]) {
+        int lo = 0, hi = kMaxExperts;  // start[lo] <= b < start[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (start[mid] <= b) lo = mid; else hi = mid;
+        }
+        owner = lo;
+      }
+      a.m_indices[b] = owner;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows of the contiguous layout that no entry fills: in the last block of each
+// expert, the rows past its count.  Row r is one when its block has an expert,
+// the next block another one, and r lies past the count's remainder.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ bool is_pad_row(int64_t row, const int32_t* m_indices, const int32_t* counts, int E,
+                                           int64_t blocks) {
+  const int64_t b = row >> 7;
+  const int e = m_indices[b];
+  if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(E)) return false;
+  if (b + 1 < blocks && m_indices[b + 1] == e) return false;
+  const int rest = counts[e] & 127;
+  return rest != 0 && static_cast<int>(row & 127) >= rest;
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch: the 1x128 quantization of each token's tiles (the same codes and
+// scales as quant_act_1x128_kernel, bit for bit), each tile written to the
+// rows of the token's slots.  A token is quantized once however many experts
+// it goes to.  Slots outside [0, rows) are skipped; pad rows of the contiguous
+// layout (m_indices given) get codes 0 and scales 1; other rows stay as they
+// are.  Eight lanes own a tile, as in the quantizer.
+// ---------------------------------------------------------------------------
+struct DispatchArgs {
+  const uint8_t* x;    // [T, D] bf16
+  const int32_t* slots;
+  int32_t top_k;
+  int32_t nkb;         // D / 128
+  int64_t num_tiles;   // T * nkb
+  int64_t rows;
+  const int32_t* m_indices;  // or null
+  const int32_t* counts;
+  int32_t E;
+  uint8_t* q;          // [rows, D]
+  float* s;            // [rows, nkb]
+};
+
+__global__ void __launch_bounds__(256, 5) moe_dispatch_1x128_kernel(DispatchArgs a) {
+  const int sub = threadIdx.x & 7;
+  const int64_t D = static_cast<int64_t>(a.nkb) * 128;
+  const int64_t grp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
+  const int64_t ngrp = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 3;
+  // same trip count for every lane of a warp (the shuffles need all 32)
+  for (int64_t t = grp; (t & ~int64_t(3)) < a.num_tiles; t += ngrp) {
+    const bool valid = t < a.num_tiles;
+    uint32_t v[8];
+    if (valid)
+      ld_nc_v8(a.x + t * 256 + sub * 32, v);
+    else
+      zero8(v);
+    float amax = abs_max16(v);
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+    const float sc = group_scale(amax);
+    const RecipPair rp = recip_pair(sc);
+    if (valid) {
+      const uint4 codes = quantize16(v, sc, rp, sc < kMinFastScale);
+      const uint32_t tok = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.nkb);
+      const uint32_t kb = static_cast<uint32_t>(t) - tok * static_cast<uint32_t>(a.nkb);
+      const int32_t* sl = a.slots + static_cast<int64_t>(tok) * a.top_k;
+      for (int j = 0; j < a.top_k; ++j) {
+        const int64_t row = __ldg(sl + j);
+        if (row >= 0 && row < a.rows) {
+          *reinterpret_cast<uint4*>(a.q + row * D + static_cast<int64_t>(kb) * 128 + sub * 16) = codes;
+          if (sub == 0) a.s[row * a.nkb + kb] = sc;
+        }
+      }
+    }
+  }
+  if (a.m_indices != nullptr) {
+    const int lane = threadIdx.x & 31;
+    const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+    for (int64_t row = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; row < a.rows;
+         row += nwarps) {
+      if (!is_pad_row(row, a.m_indices, a.counts, a.E, a.rows >> 7)) continue;
+      for (int64_t c = lane; c < D / 16; c += 32)
+        *reinterpret_cast<uint4*>(a.q + row * D + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+      for (int c = lane; c < a.nkb; c += 32) a.s[row * a.nkb + c] = 1.0f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Combine: out[t] = sum over j of w[t, j] * y[slot[t, j]] in FP32, rounded
+// once to bf16.  Without weights the plain sum: the gradient of the dispatch
+// with respect to its tokens.  Entries without a row count for nothing; a
+// token with none gets zeros.  A thread owns eight channels of a token; its
+// rows' 16-byte loads are independent of one another.
+// ---------------------------------------------------------------------------
+struct CombineArgs {
+  const uint8_t* y;      // [rows, D] bf16
+  const int32_t* slots;  // [T, top_k]
+  const float* weights;  // [T, top_k] or null
+  uint8_t* out;          // [T, D] bf16
+  int32_t top_k;
+  int32_t nkb;
+  int64_t num_tiles;     // T * nkb
+  int64_t rows;
+};
+
+// acc[0..7] += w * the eight bf16 of v.
+__device__ __forceinline__ void fma8_bf16(float (&acc)[8], const uint4& v, float w) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[2 * i] = fmaf(w, __uint_as_float(u[i] << 16), acc[2 * i]);
+    acc[2 * i + 1] = fmaf(w, __uint_as_float(u[i] & 0xFFFF0000u), acc[2 * i + 1]);
+  }
+}
+
+__global__ void __launch_bounds__(256) moe_combine_kernel(CombineArgs a) {
+  const int sub = threadIdx.x & 15;  // eight channels of a 128-channel tile
+  const int64_t stride = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 4;
+  const int64_t D = static_cast<int64_t>(a.nkb) * 128;
+  for (int64_t t = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 4; t < a.num_tiles; t += stride) {
+    const uint32_t tok = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.nkb);
+    const uint32_t kb = static_cast<uint32_t>(t) - tok * static_cast<uint32_t>(a.nkb);
+    const int64_t e0 = static_cast<int64_t>(tok) * a.top_k;
+    const int64_t col = static_cast<int64_t>(kb) * 128 + sub * 8;
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < a.top_k; ++j) {
+      const int64_t row = __ldg(a.slots + e0 + j);
+      if (row >= 0 && row < a.rows)
+        fma8_bf16(acc, ld_nc_v4(a.y + (row * D + col) * 2), a.weights != nullptr ? __ldg(a.weights + e0 + j) : 1.0f);
+    }
+    *reinterpret_cast<uint4*>(a.out + t * 256 + sub * 16) =
+        make_uint4(bf16x2_rn(acc[0], acc[1]), bf16x2_rn(acc[2], acc[3]), bf16x2_rn(acc[4], acc[5]),
+                   bf16x2_rn(acc[6], acc[7]));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the combine: dy[slot[t, j]] = bf16(w[t, j] * dout[t]) and
+// dw[t, j] = <dout[t], y[slot[t, j]]> (FP32 sums; 0 where the entry has no
+// row).  Pad rows of the contiguous layout (m_indices given) get zeros, other
+// rows stay as they are.  One CTA per token: a thread holds eight channels of
+// dout and walks the token's rows, eight entries at a time with their partial
+// dot products in registers, which are then summed over the CTA in a fixed
+// order.
+// ---------------------------------------------------------------------------
+struct CombineBwdArgs {
+  const uint8_t* dout;   // [T, D] bf16
+  const uint8_t* y;      // [rows, D] bf16
+  const int32_t* slots;
+  const float* weights;
+  uint8_t* dy;           // [rows, D] bf16
+  float* dweights;       // [T, top_k]
+  int32_t top_k;
+  int64_t T, D, rows;
+  const int32_t* m_indices;  // or null
+  const int32_t* counts;
+  int32_t E;
+};
+
+__device__ __forceinline__ float dot8_bf16(float acc, const uint4& x, const uint4& y) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), acc);
+    acc = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(v[i] & 0xFFFF0000u), acc);
+  }
+  return acc;
+}
+
+// The eight bf16 of v times w, each rounded once.
+__device__ __forceinline__ uint4 scale8_bf16(const uint4& v, float w) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = bf16x2_rn(__fmul_rn(w, __uint_as_float(u[i] << 16)), __fmul_rn(w, __uint_as_float(u[i] & 0xFFFF0000u)));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+constexpr int kCombineBwdThreads = 256;
+constexpr int kCombineBwdEntries = 8;  // entries of a token handled at once
+
+__global__ void __launch_bounds__(kCombineBwdThreads) moe_combine_bwd_kernel(CombineBwdArgs a) {
+  constexpr int kWarps = kCombineBwdThreads / 32;
+  __shared__ float part[kWarps][kCombineBwdEntries];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t chunks = a.D / 8;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const uint8_t* dout = a.dout + t * a.D * 2;
+    for (int j0 = 0; j0 < a.top_k; j0 += kCombineBwdEntries) {
+      int64_t row[kCombineBwdEntries];
+      float w[kCombineBwdEntries], acc[kCombineBwdEntries];
+#pragma unroll
+      for (int j = 0; j < kCombineBwdEntries; ++j) {
+        row[j] = -1;
+        w[j] = acc[j] = 0.0f;
+        if (j0 + j < a.top_k) {
+          const int64_t r = __ldg(a.slots + t * a.top_k + j0 + j);
+          if (r >= 0 && r < a.rows) row[j] = r;
+          w[j] = __ldg(a.weights + t * a.top_k + j0 + j);
+        }
+      }
+      for (int64_t c = tid; c < chunks; c += kCombineBwdThreads) {
+        const uint4 g = ld_nc_v4(dout + c * 16);
+#pragma unroll
+        for (int j = 0; j < kCombineBwdEntries; ++j) {
+          if (row[j] >= 0) {
+            const int64_t at = (row[j] * a.D + c * 8) * 2;
+            acc[j] = dot8_bf16(acc[j], g, ld_nc_v4(a.y + at));
+            *reinterpret_cast<uint4*>(a.dy + at) = scale8_bf16(g, w[j]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kCombineBwdEntries; ++j) {
+        const float s = warp_sum(acc[j]);
+        if (lane == 0) part[warp][j] = s;
+      }
+      __syncthreads();
+      if (tid < kCombineBwdEntries && j0 + tid < a.top_k) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) s += part[i][tid];
+        a.dweights[t * a.top_k + j0 + tid] = s;
+      }
+      __syncthreads();
+    }
+  }
+  if (a.m_indices != nullptr) {
+    const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp; row < a.rows; row += nwarps) {
+      if (!is_pad_row(row, a.m_indices, a.counts, a.E, a.rows >> 7)) continue;
+      for (int64_t c = lane; c < chunks; c += 32)
+        *reinterpret_cast<uint4*>(a.dy + (row * a.D + c * 8) * 2) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+}
+
+}  // namespace fp8q

@@ -301,6 +301,157 @@ FP8Q_API int fp8_grouped_gemm_mx_masked(const uint8_t* qa, const uint8_t* sfa_mx
 FP8Q_API int fp8_gemm_unpromoted_diag(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb, void* c_bf16,
                              int64_t M, int64_t N, int64_t K, cudaStream_t stream);
 
+/*
+ * Mixture-of-experts routing: which experts a token goes to, and with what
+ * weights (the choice that the grouped layouts of the DeepGEMM page, "Principais
+ * caracteristicas", take as given).  For each token, over its E logits l:
+ *   score   p = softmax(l), or 1 / (1 + exp(-l)) with sigmoid;
+ *   key     p + bias where a bias is given (a load-balancing bias moves the
+ *           choice, not the weights), else p;
+ *   groups  with n_group > 1 the E / n_group consecutive experts of a group
+ *           share the sum of the group's best group_top (1 or 2) keys, and the
+ *           topk_group groups with the largest sums stay;
+ *   choice  the top_k largest keys among the experts that stay, largest first;
+ *   weight  scale * p, or with renorm scale * p / (sum of the chosen p).
+ * Keys are compared as binary64 values of these expressions; equal keys, and
+ * equal groups, go to the lower index.  An expert whose logit or bias is -inf
+ * or NaN is never chosen; a place that finds no expert (a row whose mask leaves
+ * fewer than top_k) gets id -1 and weight 0, and renorm runs over the others.
+ * A logit of +inf counts as the largest finite float.
+ *   logits  : [T, E] f32, or bf16 with logits_bf16 != 0, read only.
+ *   bias    : [E] f32 or NULL.
+ *   ids     : [T, top_k] int32, written.  weights : [T, top_k] f32, written.
+ * 1 <= E <= 1024, n_group <= 32 divides E, 1 <= topk_group <= n_group,
+ * 1 <= top_k <= 32 and top_k <= topk_group * E / n_group.  T == 0: no-op.
+ * Pointers aligned to their element.
+ */
+FP8Q_API int fp8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t E, const float* bias, int sigmoid,
+                           int64_t top_k, int64_t n_group, int64_t topk_group, int64_t group_top, int renorm,
+                           float scale, int32_t* ids, float* weights, cudaStream_t stream);
+
+/*
+ * Gradient of fp8_moe_route's weights with respect to the logits, the choice
+ * held constant (the bias gets none: it does not enter the weights).
+ *   ids      : [T, top_k] int32; entries outside [0, E) count for nothing, an
+ *              id that appears twice in a row gets the sum.
+ *   dweights : [T, top_k] f32.
+ *   dlogits  : [T, E], the logits' type, every element written (0 for experts
+ *              with no part in the weights, and for logits of -inf or NaN).
+ * E, top_k, T as above.
+ */
+FP8Q_API int fp8_moe_route_bwd(const void* logits, int logits_bf16, int64_t T, int64_t E, const int32_t* ids,
+                               const float* dweights, int sigmoid, int64_t top_k, int renorm, float scale,
+                               void* dlogits, cudaStream_t stream);
+
+/*
+ * Row layouts of the grouped GEMMs for chosen experts.  Entry (t, j) of ids
+ * gets a row of the expert-major buffers, in entry order within each expert (so
+ * the layout is a function of ids alone); ids outside [0, E) get none (-1).
+ *
+ * Contiguous: each expert's run starts on a 128-row block, experts ascending.
+ *   slots     : [T, top_k] int32, written: row of each entry, or -1.
+ *   m_indices : [B] int32, written: expert of each 128-row block, -1 for blocks
+ *               past the last (the grouped GEMM skips them).  B = (n + 127 *
+ *               min(n, E)) / 128 rounded down, n = T * top_k: the most blocks
+ *               that n entries can need, so the host need not know the counts.
+ *   counts    : [E] int32, written: entries of each expert.
+ * Masked: row expert * cap + rank; entries whose rank reaches cap get -1.
+ *   masked_m  : [E] int32, written: min(entries, cap) of each expert.
+ * 1 <= E <= 1024, 1 <= top_k <= 32, cap a positive multiple of 128, rows below
+ * 2^31.  With T == 0 the counts are still written.  Pointers 4-byte aligned.
+ */
+FP8Q_API int fp8_moe_layout_contiguous(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* slots,
+                                       int32_t* m_indices, int32_t* counts, cudaStream_t stream);
+FP8Q_API int fp8_moe_layout_masked(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int64_t cap,
+                                   int32_t* slots, int32_t* masked_m, cudaStream_t stream);
+
+/*
+ * Dispatch of tokens to expert rows, fused with the 1x128 quantization: row
+ * slots[t, j] of q and s gets exactly fp8_quant_act_1x128's codes and scales of
+ * token t, for every j with a slot in [0, rows).  The valid slots are distinct
+ * (as the layouts above give them).
+ *   x_bf16 : [T, D] bf16.  slots : [T, top_k] int32.
+ *   q : [rows, D] E4M3, s : [rows, D/128] f32, written where a slot points.
+ *   m_indices [rows/128], counts [E] : both NULL, or the contiguous layout's;
+ *            then the rows that pad an expert's last block get codes 0 and
+ *            scale 1 (rows a multiple of 128).
+ * Other rows (past masked_m, blocks past the last) are left as they were.
+ * D a multiple of 128, T * D / 128 below 2^31.  x 32-byte, q 16-byte, the
+ * others 4-byte aligned.
+ */
+FP8Q_API int fp8_moe_dispatch_1x128(const void* x_bf16, int64_t T, int64_t D, const int32_t* slots, int64_t top_k,
+                                    int64_t rows, const int32_t* m_indices, const int32_t* counts, int64_t E,
+                                    uint8_t* q, float* s, cudaStream_t stream);
+
+/*
+ * Combine of the experts' outputs: out[t] = bf16_rne( sum_j weights[t, j] *
+ * y[slots[t, j]] ), FP32 sums in the order of j.  With weights NULL the plain
+ * sum: the gradient of the dispatch with respect to its tokens.  Entries whose
+ * slot lies outside [0, rows) count for nothing (their y is not read); a token
+ * with none gets zeros.
+ *   y_bf16 : [rows, D] bf16.  out_bf16 : [T, D] bf16, every element written.
+ * Sizes as above; y and out 16-byte, slots and weights 4-byte aligned.
+ */
+FP8Q_API int fp8_moe_combine(const void* y_bf16, int64_t rows, int64_t D, const int32_t* slots, const float* weights,
+                             int64_t T, int64_t top_k, void* out_bf16, cudaStream_t stream);
+
+/*
+ * Gradient of the combine:
+ *   dy_bf16  : [rows, D] bf16; row slots[t, j] gets bf16_rne(weights[t, j] *
+ *              dout[t]).  With m_indices and counts the contiguous layout's pad
+ *              rows get zeros; other rows are left as they were.
+ *   dweights : [T, top_k] f32: <dout[t], y[slots[t, j]]>, 0 without a slot.
+ *   dout_bf16 : [T, D] bf16.  weights : [T, top_k] f32 (required).
+ * The valid slots are distinct.  dy may not overlap y.
+ */
+FP8Q_API int fp8_moe_combine_bwd(const void* dout_bf16, const void* y_bf16, int64_t rows, int64_t D,
+                                 const int32_t* slots, const float* weights, int64_t T, int64_t top_k,
+                                 const int32_t* m_indices, const int32_t* counts, int64_t E, void* dy_bf16,
+                                 float* dweights, cudaStream_t stream);
+
+/*
+ * Activation checkpoints in 8 bits ("The Insider Secrets Of Deepseek
+ * Discovered", Figure 6: the operands of all three GEMMs are FP8; what the
+ * forward pass quantized is kept for the backward pass in place of bf16).
+ *
+ * SwiGLU with its checkpoint, one pass over c1 = [gate | up]:
+ *   qh, sh : exactly fp8_swiglu_quant_1x128(c1) (the next GEMM's activation),
+ *   qc, sc : exactly fp8_quant_act_1x128(c1), [rows, 2*inter] codes and
+ *            [rows, 2*inter/128] scales: all that fp8_swiglu_bwd_1x128 needs.
+ * inter a multiple of 128, rows * inter / 128 below 2^31.  c1 32-byte, qh and
+ * qc 16-byte, sh and sc 4-byte aligned.
+ */
+FP8Q_API int fp8_swiglu_ckpt_1x128(const void* c1_bf16, int64_t rows, int64_t inter, uint8_t* qh, float* sh,
+                                   uint8_t* qc, float* sc, cudaStream_t stream);
+
+/*
+ * SwiGLU backward from the checkpoint: with g and u = fl32(qc * sc) of the two
+ * halves and p = 1 / (1 + exp(-g)), in FP32,
+ *   d = [ dh u p (1 + g (1 - p)) | dh g p ]
+ *   dh_bf16 : [rows, inter] bf16.
+ *   dc_bf16 : [rows, 2*inter] bf16, written: bf16_rne(d).
+ *   q, s    : [rows, 2*inter] E4M3, [rows, 2*inter/128] f32, written: the 1x128
+ *             quantization of the FP32 values d (not of their bf16 rounding),
+ *             the operand of the activation gradient's GEMM.
+ * Sizes as above; dh 32-byte, dc, qc and q 16-byte, sc and s 4-byte aligned.
+ */
+FP8Q_API int fp8_swiglu_bwd_1x128(const void* dh_bf16, const uint8_t* qc, const float* sc, int64_t rows, int64_t inter,
+                                  void* dc_bf16, uint8_t* q, float* s, cudaStream_t stream);
+
+/*
+ * Weight-gradient operand from a checkpoint: 1x128 tiles regrouped along
+ * tokens, the layout of fp8_quant_act_128x1_t.  The values fl32(q * s) are
+ * quantized per 128 tokens x 1 channel by the rule above (s = fl32(amax / 448),
+ * 1 for an all-zero group; codes of fl32(v / s)).
+ *   q  : [M, K] E4M3, s : [M, K/128] f32 (any 1x128 quantization).
+ *   qt : [K, Mp] E4M3, written; code 0 for tokens at or past M.
+ *   st : [Mp/128, K] f32, written.
+ * K and Mp multiples of 128, Mp >= M (fp8_gemm_wgrad takes multiples of 512).
+ * q, qt and st 16-byte, s 4-byte aligned.
+ */
+FP8Q_API int fp8_ckpt_128x1_t(const uint8_t* q, const float* s, int64_t M, int64_t K, int64_t Mp, uint8_t* qt,
+                              float* st, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 FP8Q_API const char* fp8q_status_string(int status);
 
