@@ -33,6 +33,7 @@ Names and semantics match the C entry points:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from pathlib import Path
 
@@ -132,10 +133,24 @@ def _check(rc: int, what: str):
         raise Fp8qError(rc, what)
 
 
+# The handle of a device's current stream without building a torch.cuda.Stream for it (2 us of a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device) -> int:
     if stream is None:
+        if _raw_stream is not None and device.index is not None:
+            return _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_STAY = contextlib.nullcontext()
+
+
+def _on(device):
+    """Makes `device` current for a call; nothing to do where it is already."""
+    return _STAY if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _tensor(t, name: str, dtypes, ndim=None):
@@ -206,7 +221,7 @@ def fp8_quant_act_1x128(x: torch.Tensor, q: torch.Tensor | None = None, s: torch
         q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
     if s is None:
         s = torch.empty((M, K // TILE), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(getattr(lib(), _entry)(_p(x), M, K, _p(q), _p(s), _stream(stream, dev)), _entry)
     return q, s
 
@@ -228,7 +243,7 @@ def fp8_quant_w_128x128(w: torch.Tensor, q: torch.Tensor | None = None, s: torch
         q = torch.empty(tuple(w.shape), dtype=torch.float8_e4m3fn, device=dev)
     if s is None:
         s = torch.empty(lead + (N // TILE, K // TILE), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(getattr(lib(), _entry)(_p(w), G, N, K, _p(q), _p(s), _stream(stream, dev)), _entry)
     return q, s
 
@@ -259,7 +274,7 @@ def fp8_quant_act_w(x: torch.Tensor, w: torch.Tensor, qa: torch.Tensor | None = 
         qw = torch.empty(tuple(w.shape), dtype=torch.float8_e4m3fn, device=dev)
     if sw is None:
         sw = torch.empty(tuple(w.shape[:-2]) + (N // TILE, Kw // TILE), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_quant_act_w(_p(x), M, K, _p(qa), _p(sa), _p(w), G, N, Kw, _p(qw), _p(sw),
                                      _stream(stream, dev)), "fp8_quant_act_w")
     return (qa, sa), (qw, sw)
@@ -290,7 +305,7 @@ def fp8_quant_act_128x1(x: torch.Tensor, q: torch.Tensor | None = None, s: torch
         q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
     if s is None:
         s = torch.empty((nmb, K), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_quant_act_128x1(_p(x), M, K, _p(q), _p(s), _stream(stream, dev)), "fp8_quant_act_128x1")
     return q, s
 
@@ -320,7 +335,7 @@ def fp8_quant_act_128x1_t(x: torch.Tensor, qt: torch.Tensor | None = None, s: to
         qt = torch.empty((K, Mp), dtype=torch.float8_e4m3fn, device=dev)
     if s is None:
         s = torch.empty((Mp // TILE, K), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_quant_act_128x1_t(_p(x), M, K, Mp, _p(qt), _p(s), _stream(stream, dev)),
                "fp8_quant_act_128x1_t")
     return qt, s
@@ -346,7 +361,7 @@ def fp8_transpose_w_128x128(q: torch.Tensor, s: torch.Tensor, qt: torch.Tensor |
         qt = torch.empty(lead + (K, N), dtype=torch.float8_e4m3fn, device=dev)
     if st is None:
         st = torch.empty(lead + (K // TILE, N // TILE), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_transpose_w_128x128(_p(q), _p(s), G, N, K, _p(qt), _p(st), _stream(stream, dev)),
                "fp8_transpose_w_128x128")
     return qt, st
@@ -381,7 +396,7 @@ def fp8_swiglu_quant_1x128(c1: torch.Tensor, masked_m: torch.Tensor | None = Non
         qh = torch.empty(lead + (inter,), dtype=torch.float8_e4m3fn, device=dev)
     if sh is None:
         sh = torch.empty(lead + (inter // TILE,), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_swiglu_quant_1x128(_p(c1), rows, inter, _p(masked_m), cap, _p(qh), _p(sh),
                                             _stream(stream, dev)), "fp8_swiglu_quant_1x128")
     return qh, sh
@@ -411,7 +426,7 @@ def fp8_gemm_blockscaled(qa, sa, qb, sb, out: torch.Tensor | None = None, stream
     M, N, K, dev = _dense_operands(qa, sa, qb, sb, out)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_gemm_blockscaled(_p(qa), _p(sa), _p(qb), _p(sb), _p(out), M, N, K,
                                           _stream(stream, dev)), "fp8_gemm_blockscaled")
     return out
@@ -422,7 +437,7 @@ def fp8_gemm_unpromoted_diag(qa, sa, qb, sb, out: torch.Tensor | None = None, st
     M, N, K, dev = _dense_operands(qa, sa, qb, sb, out)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_gemm_unpromoted_diag(_p(qa), _p(sa), _p(qb), _p(sb), _p(out), M, N, K,
                                               _stream(stream, dev)), "fp8_gemm_unpromoted_diag")
     return out
@@ -451,7 +466,7 @@ def fp8_gemm_wgrad(q_dy_t, s_dy, q_x_t, s_x, out: torch.Tensor | None = None, st
     dev = _device_of(q_dy_t=q_dy_t, s_dy=s_dy, q_x_t=q_x_t, s_x=s_x, out=out)
     if out is None:
         out = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_gemm_wgrad(_p(q_dy_t), _p(s_dy), _p(q_x_t), _p(s_x), _p(out), N, K, Mp,
                                     _stream(stream, dev)), "fp8_gemm_wgrad")
     return out
@@ -470,7 +485,7 @@ def fp8_mx_scales_act(sa: torch.Tensor, out: torch.Tensor | None = None, stream=
     dev = _device_of(sa=sa, out=out)
     if out is None:
         out = torch.empty((mt, nkb, MX_ATOM), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_mx_scales_act(_p(sa), M, nkb * TILE, _p(out), _stream(stream, dev)), "fp8_mx_scales_act")
     return out
 
@@ -484,7 +499,7 @@ def fp8_mx_scales_w(sb: torch.Tensor, out: torch.Tensor | None = None, stream=No
     dev = _device_of(sb=sb, out=out)
     if out is None:
         out = torch.empty((G * nnb, nkb, MX_ATOM), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_mx_scales_w(_p(sb), G, nnb * TILE, nkb * TILE, _p(out), _stream(stream, dev)),
                "fp8_mx_scales_w")
     return out
@@ -510,7 +525,7 @@ def fp8_gemm_mx(qa, sfa_mx, qb, sfb_mx, out: torch.Tensor | None = None, stream=
     dev = _device_of(qa=qa, sfa_mx=sfa_mx, qb=qb, sfb_mx=sfb_mx, out=out)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_gemm_mx(_p(qa), _p(sfa_mx), _p(qb), _p(sfb_mx), _p(out), M, N, K, _stream(stream, dev)),
                "fp8_gemm_mx")
     return out
@@ -539,7 +554,7 @@ def fp8_grouped_gemm_mx_contiguous(qa, sfa_mx, qb, sfb_mx, m_indices, out: torch
     dev = _device_of(qa=qa, sfa_mx=sfa_mx, qb=qb, sfb_mx=sfb_mx, m_indices=m_indices, out=out)
     if out is None:
         out = torch.empty((M_tot, N), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_grouped_gemm_mx_contiguous(_p(qa), _p(sfa_mx), _p(qb), _p(sfb_mx), _p(m_indices), _p(out),
                                                     M_tot, N, K, E, _stream(stream, dev)),
                "fp8_grouped_gemm_mx_contiguous")
@@ -569,7 +584,7 @@ def fp8_grouped_gemm_mx_masked(qa, sfa_mx, qb, sfb_mx, masked_m, out: torch.Tens
     dev = _device_of(qa=qa, sfa_mx=sfa_mx, qb=qb, sfb_mx=sfb_mx, masked_m=masked_m, out=out)
     if out is None:
         out = torch.empty((E, cap, N), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_grouped_gemm_mx_masked(_p(qa), _p(sfa_mx), _p(qb), _p(sfb_mx), _p(masked_m), _p(out), E,
                                                 cap, N, K, _stream(stream, dev)), "fp8_grouped_gemm_mx_masked")
     return out
@@ -599,7 +614,7 @@ def fp8_grouped_gemm_contiguous(qa, sa, qb, sb, m_indices, out: torch.Tensor | N
     dev = _device_of(qa=qa, sa=sa, qb=qb, sb=sb, m_indices=m_indices, out=out)
     if out is None:
         out = torch.empty((M_tot, N), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_grouped_gemm_contiguous(_p(qa), _p(sa), _p(qb), _p(sb), _p(m_indices), _p(out), M_tot, N, K,
                                                  E, _stream(stream, dev)), "fp8_grouped_gemm_contiguous")
     return out
@@ -630,7 +645,7 @@ def fp8_grouped_gemm_masked(qa, sa, qb, sb, masked_m, expected_m: int = 0, out: 
     dev = _device_of(qa=qa, sa=sa, qb=qb, sb=sb, masked_m=masked_m, out=out)
     if out is None:
         out = torch.empty((E, cap, N), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_grouped_gemm_masked(_p(qa), _p(sa), _p(qb), _p(sb), _p(masked_m), _p(out), E, cap, N, K,
                                              int(expected_m), _stream(stream, dev)), "fp8_grouped_gemm_masked")
     return out
@@ -691,7 +706,7 @@ def fp8_moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = 
         ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     if weights is None:
         weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_moe_route(_p(logits), logits.dtype == torch.bfloat16, T, E, _p(bias), sig, top_k, n_group,
                                    topk_group, group_top, bool(renorm), float(scale), _p(ids), _p(weights),
                                    _stream(stream, dev)), "fp8_moe_route")
@@ -714,7 +729,7 @@ def fp8_moe_route_bwd(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.T
     dev = _device_of(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
     if dlogits is None:
         dlogits = torch.empty_like(logits)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_moe_route_bwd(_p(logits), logits.dtype == torch.bfloat16, T, E, _p(ids), _p(dweights), sig,
                                        top_k, bool(renorm), float(scale), _p(dlogits), _stream(stream, dev)),
                "fp8_moe_route_bwd")
@@ -758,7 +773,7 @@ def fp8_moe_layout_contiguous(ids: torch.Tensor, E: int, slots: torch.Tensor | N
         m_indices = torch.empty((B,), dtype=torch.int32, device=dev)
     if counts is None:
         counts = torch.empty((E,), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_moe_layout_contiguous(_p(ids), T, top_k, E, _p(slots), _p(m_indices), _p(counts),
                                                _stream(stream, dev)), "fp8_moe_layout_contiguous")
     return slots, m_indices, counts
@@ -782,7 +797,7 @@ def fp8_moe_layout_masked(ids: torch.Tensor, E: int, cap: int, slots: torch.Tens
         slots = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     if masked_m is None:
         masked_m = torch.empty((E,), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_moe_layout_masked(_p(ids), T, top_k, E, cap, _p(slots), _p(masked_m), _stream(stream, dev)),
                "fp8_moe_layout_masked")
     return slots, masked_m
@@ -835,7 +850,7 @@ def fp8_moe_dispatch_1x128(x: torch.Tensor, slots: torch.Tensor, rows: int, m_in
         q = torch.empty((rows, D), dtype=torch.float8_e4m3fn, device=dev)
     if s is None:
         s = torch.empty((rows, D // TILE), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_moe_dispatch_1x128(_p(x), T, D, _p(slots), top_k, rows, _p(m_indices), _p(counts), E, _p(q),
                                             _p(s), _stream(stream, dev)), "fp8_moe_dispatch_1x128")
     return q, s
@@ -865,7 +880,7 @@ def fp8_moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor 
     dev = _device_of(y=y, slots=slots, weights=weights, out=out)
     if out is None:
         out = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_moe_combine(_p(y), rows, D, _p(slots), _p(weights), T, top_k, _p(out),
                                      _stream(stream, dev)), "fp8_moe_combine")
     return out
@@ -900,7 +915,7 @@ def fp8_moe_combine_bwd(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tensor
         raise ValueError("dy may not be y: its rows are read while dy is written")
     if dweights is None:
         dweights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_moe_combine_bwd(_p(dout), _p(y), rows, D, _p(slots), _p(weights), T, top_k, _p(m_indices),
                                          _p(counts), E, _p(dy), _p(dweights), _stream(stream, dev)),
                "fp8_moe_combine_bwd")
@@ -933,7 +948,7 @@ def fp8_swiglu_ckpt_1x128(c1: torch.Tensor, qh: torch.Tensor | None = None, sh: 
         qc = torch.empty((rows, 2 * inter), dtype=torch.float8_e4m3fn, device=dev)
     if sc is None:
         sc = torch.empty((rows, 2 * (inter // TILE)), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_swiglu_ckpt_1x128(_p(c1), rows, inter, _p(qh), _p(sh), _p(qc), _p(sc),
                                            _stream(stream, dev)), "fp8_swiglu_ckpt_1x128")
     return (qh, sh), (qc, sc)
@@ -969,7 +984,7 @@ def fp8_swiglu_bwd_1x128(dh: torch.Tensor, qc: torch.Tensor, sc: torch.Tensor, d
         q = torch.empty((rows, 2 * inter), dtype=torch.float8_e4m3fn, device=dev)
     if s is None:
         s = torch.empty((rows, 2 * (inter // TILE)), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_swiglu_bwd_1x128(_p(dh), _p(qc), _p(sc), rows, inter, _p(dc), _p(q), _p(s),
                                           _stream(stream, dev)), "fp8_swiglu_bwd_1x128")
     return dc, (q, s)
@@ -999,7 +1014,7 @@ def fp8_ckpt_128x1_t(q: torch.Tensor, s: torch.Tensor, Mp: int | None = None, qt
         qt = torch.empty((K, Mp), dtype=torch.float8_e4m3fn, device=dev)
     if st is None:
         st = torch.empty((Mp // TILE, K), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib().fp8_ckpt_128x1_t(_p(q), _p(s), M, K, Mp, _p(qt), _p(st), _stream(stream, dev)),
                "fp8_ckpt_128x1_t")
     return qt, st

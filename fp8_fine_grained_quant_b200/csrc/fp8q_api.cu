@@ -774,6 +774,37 @@ int fp8_gemm_wgrad(const uint8_t* q_dy_t, const float* s_dy, const uint8_t* q_x_
 }
 
 // ---------------------------------------------------------------- mixture of experts
+}  // extern "C"
+
+// The router's kernel for a shape: a group gets a power of two of lanes, at
+// most 32 / n_group, each lane an equal share of the group's experts, and the
+// instance is the least that holds the share.  Shares above 32 (over 16
+// groups, not a power of two, of over 32 experts) take the binary64 kernel.
+template <bool kBf16>
+static void launch_route(const RouteArgs& a, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>((a.T + kRouteWarps - 1) / kRouteWarps);
+  const unsigned block = 32 * kRouteWarps;
+  const size_t smem = static_cast<size_t>(kRouteWarps) * a.E * sizeof(double);
+  const int size = a.E / a.n_group;
+  RouteSplit sp{32, 0, 0};
+  while (sp.lanes * a.n_group > 32) sp.lanes /= 2;
+  sp.per_lane = (size + sp.lanes - 1) / sp.lanes;
+  int vpl = 1;
+  while (vpl < sp.per_lane) vpl *= 2;
+  sp.vector = a.E == 32 * vpl && sp.lanes * sp.per_lane == size && aligned(a.logits, 16);
+  switch (vpl) {
+    case 1: moe_route_kernel<1, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
+    case 2: moe_route_kernel<2, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
+    case 4: moe_route_kernel<4, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
+    case 8: moe_route_kernel<8, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
+    case 16: moe_route_kernel<16, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
+    case 32: moe_route_kernel<32, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
+    default: moe_route_f64_kernel<kBf16><<<grid, block, smem, stream>>>(a);
+  }
+}
+
+extern "C" {
+
 // Sizes shared by the routing, layout, dispatch and combine entry points: a
 // token's experts are one lane of a warp each, and the kernels number tokens'
 // tiles in 32 bits.
@@ -814,12 +845,10 @@ int fp8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t E, con
   RouteArgs a{logits, bias, ids, weights, T, static_cast<int32_t>(E), static_cast<int32_t>(top_k),
               static_cast<int32_t>(n_group), static_cast<int32_t>(topk_group), static_cast<int32_t>(group_top),
               sigmoid != 0, renorm != 0, scale};
-  const unsigned grid = static_cast<unsigned>((T + kRouteWarps - 1) / kRouteWarps);
-  const size_t smem = static_cast<size_t>(kRouteWarps) * E * sizeof(double);
   if (logits_bf16)
-    moe_route_kernel<true><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
+    launch_route<true>(a, stream);
   else
-    moe_route_kernel<false><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
+    launch_route<false>(a, stream);
   return launched();
 }
 

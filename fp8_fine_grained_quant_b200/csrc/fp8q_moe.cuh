@@ -40,9 +40,10 @@ __device__ __forceinline__ float warp_max(float v) {
 // ---------------------------------------------------------------------------
 // Expert choice.  For each token with logits l over E experts:
 //   score   p_e = softmax(l)_e or 1 / (1 + exp(-l_e));
-//   key     p_e + bias_e with a bias, else p_e (the order of l_e itself);
-//   groups  the E / n_group experts of a group share the sum of the group's
-//           best one or two keys; the topk_group best groups stay;
+//   key     p_e + bias_e with a bias, else p_e; where single experts are
+//           compared without a bias, l_e itself (the same order);
+//   groups  the E / n_group experts of a group share the group's best key or
+//           the sum of its best two; the topk_group best groups stay;
 //   choice  the top_k best keys of the experts that stay, best first;
 //   weights scale * p_e, or scale * p_e / sum of the chosen p (renorm): the
 //           bias moves the choice, not the weights.
@@ -122,7 +123,7 @@ __device__ __noinline__ int route_choose_f64(const RouteArgs& a, const void* row
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
   }
-  const bool by_score = a.bias != nullptr || a.n_group > 1;
+  const bool by_score = a.bias != nullptr || (a.n_group > 1 && a.group_top == 2);
   for (int e = lane; e < E; e += 32) {
     const float l = load_logit<kBf16>(row, e);
     double k = static_cast<double>(l);
@@ -158,7 +159,7 @@ __device__ __noinline__ int route_choose_f64(const RouteArgs& a, const void* row
     for (int e = lane; e < E; e += 32) {
       if (!((keep >> (e / size)) & 1u))
         keys[e] = neg_inf_f64();
-      else if (a.bias == nullptr)
+      else if (by_score && a.bias == nullptr)
         keys[e] = static_cast<double>(load_logit<kBf16>(row, e));
     }
     __syncwarp();
@@ -190,10 +191,272 @@ __device__ __noinline__ int route_choose_f64(const RouteArgs& a, const void* row
   return mine;
 }
 
+// Order-preserving map of FP32 to uint32 and back; 0 is below every finite
+// value and stands for "never chosen".
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+__device__ __forceinline__ uint32_t redux_max(uint32_t v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
+__device__ __forceinline__ uint32_t redux_min(uint32_t v) { return __reduce_min_sync(0xFFFFFFFFu, v); }
+
+// N values in descending order, by an odd-even merge network (N a power of two).
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1) {
+#pragma unroll
+    for (int q = p; q >= 1; q >>= 1) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (i + q < N && i >= q % p && (i - q % p) / q % 2 == 0 && i / (2 * p) == (i + q) / (2 * p)) {
+          const uint32_t x = v[i], y = v[i + q < N ? i + q : i];
+          v[i] = max(x, y);
+          v[i + q < N ? i + q : i] = min(x, y);
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// How the experts of a row lie over a warp: the lanes of group g are
+// g * lanes .. + lanes - 1, each with `per_lane` consecutive experts of the
+// group, so lane order is expert order.  With one group: 32 lanes.
+struct RouteSplit {
+  int32_t lanes;     // of a group, a power of two
+  int32_t per_lane;  // at most the kernel's VPL
+  int32_t vector;    // the lanes' runs tile the row and are aligned: vector loads
+};
+
+// A lane's logits l[i] (expert base + i), -inf past its share.
+template <int VPL, bool kBf16>
+__device__ __forceinline__ void load_share(const void* row, int base, int count, bool vector, float (&l)[VPL]) {
+  constexpr int kBytes = VPL * (kBf16 ? 2 : 4);
+  if (kBytes >= 4 && vector) {
+    constexpr int kWords = kBytes >= 4 ? kBytes / 4 : 1;
+    uint32_t w[kWords];
+    const uint8_t* p = static_cast<const uint8_t*>(row) + static_cast<int64_t>(base) * (kBf16 ? 2 : 4);
+    if constexpr (kWords >= 4) {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
+      }
+    } else if constexpr (kWords == 2) {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = x.x;
+      w[1] = x.y;
+    } else {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if constexpr (kBf16)
+        l[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
+      else
+        l[i] = __uint_as_float(w[i < kWords ? i : 0]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      l[i] = neg_inf_f32();
+      if (i < count) {
+        if constexpr (kBf16)
+          l[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(row)[base + i]);
+        else
+          l[i] = static_cast<const float*>(row)[base + i];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) l[i] = l[i] > neg_inf_f32() ? fminf(l[i], FLT_MAX) : neg_inf_f32();
+}
+
 constexpr int kRouteWarps = 4;
 
+// The common case in FP32, with a proof: a warp holds its row in registers,
+// each lane its share's keys in descending order.  A round of the choice takes
+// the largest of the lanes' heads (one warp reduction); the lowest lane that
+// has it gives it up.
+//
+// Without a bias experts are compared by their logits, exactly.  With one, and
+// for group sums, FP32 keys are compared, and each comparison that decides
+// (neighbours in the choice, the first expert left out, the worst group kept
+// against the best one dropped) must be wider than the keys' error; a row
+// where one is not goes to route_choose_f64.  Equal keys of equal logits and
+// biases need no proof.  The errors, with __expf off by (2 + 1.173 |x|) ulp:
+//   sigmoid  p (1 - p) (2 + 1.173 |x|) 2^-23 <= 2^-23, + 2^-23 (1 + e) and rcp:
+//            below 2^-21.6 a key; + 2^-24 |key| from adding the bias;
+//   softmax  at most 30 * 2^-23 of p from the row's sum (37 additions, and
+//            sum p |x| <= ln 1024), and 3 * 2^-23: below 2^-17.9 for any two
+//            keys, as their p sum to at most 1;
+// so two keys further apart than 2^-20 (sigmoid) or 2^-17 (softmax) + 2^-22 of
+// the larger are in order; for sums of two keys, twice that.
+template <int VPL, bool kBf16>
+__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(RouteArgs a, RouteSplit sp) {
+  extern __shared__ double route_keys[];  // [kRouteWarps][E]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
+  if (t >= a.T) return;
+  const void* row = logits_row<kBf16>(a.logits, t, a.E);
+  const int size = a.E / a.n_group;
+  const int g = lane / sp.lanes;
+  const int first = (lane & (sp.lanes - 1)) * sp.per_lane;
+  const int base = g * size + first;
+  const int count = g < a.n_group ? max(0, min(sp.per_lane, size - first)) : 0;
+  float l[VPL];
+  load_share<VPL, kBf16>(row, base, count, sp.vector, l);
+
+  // softmax statistics of the row, where something needs them
+  const bool pair_sums = a.n_group > 1 && a.group_top == 2;
+  float row_max = neg_inf_f32(), row_sum = 0.0f;
+  if (!a.sigmoid && (a.bias != nullptr || pair_sums || !a.renorm)) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) row_max = fmaxf(row_max, l[i]);
+    row_max = warp_max(row_max);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (l[i] > neg_inf_f32()) row_sum += a.renorm ? __expf(l[i] - row_max) : expf(l[i] - row_max);
+    }
+    row_sum = warp_sum(row_sum);
+  }
+  const float inv_sum = rcp_approx(row_sum);
+  auto score = [&](float x) {
+    return a.sigmoid ? rcp_approx(1.0f + __expf(-x)) : __expf(x - row_max) * inv_sum;
+  };
+
+  // keys: the logits, or score + bias
+  uint32_t key[VPL], s[VPL];
+  if (a.bias == nullptr) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = l[i] > neg_inf_f32() ? key_of(l[i] + 0.0f) : 0u;  // -0 as +0
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const float b = i < count ? __ldg(a.bias + base + i) : 0.0f;
+      key[i] = l[i] > neg_inf_f32() && b > neg_inf_f32() ? key_of(score(l[i]) + b + 0.0f) : 0u;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) s[i] = key[i];
+  sort_descending<VPL>(s);
+
+  const float tol = a.sigmoid ? 0x1p-20f : 0x1p-17f;
+  bool certain = true;
+  if (a.n_group > 1) {
+    // the group's best one or two, in every lane of the group
+    uint32_t b1 = s[0], b2 = VPL > 1 ? s[VPL > 1 ? 1 : 0] : 0u;
+    for (int off = 1; off < sp.lanes; off <<= 1) {
+      const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, off), o2 = __shfl_xor_sync(0xFFFFFFFFu, b2, off);
+      b2 = max(min(b1, o1), max(b2, o2));
+      b1 = max(b1, o1);
+    }
+    uint32_t total = b1;  // group_top 1: the best key decides
+    const bool exact = a.group_top == 1 && a.bias == nullptr;
+    if (a.group_top == 2) {
+      float v1 = value_of(b1), v2 = value_of(b2);
+      if (a.bias == nullptr) {
+        v1 = score(v1);
+        v2 = score(v2);
+      }
+      total = b1 == 0u ? 0u : key_of(b2 == 0u ? v1 : v1 + v2);
+    }
+    int ahead = 0;
+    for (int h = 0; h < a.n_group; ++h) {
+      const uint32_t o = __shfl_sync(0xFFFFFFFFu, total, h * sp.lanes);
+      ahead += o > total || (o == total && h < g);
+    }
+    const bool in = g < a.n_group, keep = in && ahead < a.topk_group;
+    if (!exact && a.topk_group < a.n_group) {
+      const uint32_t worst = redux_min(keep ? total : 0xFFFFFFFFu), best = redux_max(in && !keep ? total : 0u);
+      const float w = value_of(worst), b = value_of(best);
+      certain = best == 0u || w - b > 2.0f * tol + 0x1p-20f * fmaxf(fabsf(w), fabsf(b));
+    }
+    if (!keep) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s[i] = 0u;
+    }
+  }
+
+  // the choice: lane j gets place j's key, the lane that had it, and how many
+  // equal keys of that lane went before it
+  const bool prove = a.bias != nullptr;
+  const int rounds = a.top_k + (prove && a.top_k < 32 ? 1 : 0);
+  uint32_t my_key = 0u, last_key = 0u;
+  int my_lane = 0, my_rep = 0, last_lane = -1, rep = 0;
+  for (int j = 0; j < rounds; ++j) {
+    const uint32_t m = redux_max(s[0]);
+    if (m == 0u) break;
+    const int w = __ffs(__ballot_sync(0xFFFFFFFFu, s[0] == m)) - 1;
+    rep = m == last_key && w == last_lane ? rep + 1 : 0;
+    last_key = m;
+    last_lane = w;
+    if (lane == j) {
+      my_key = m;
+      my_lane = w;
+      my_rep = rep;
+    }
+    if (lane == w) {
+#pragma unroll
+      for (int i = 0; i + 1 < VPL; ++i) s[i] = s[i + 1];
+      s[VPL - 1] = 0u;
+    }
+  }
+  int at = 0, seen = my_rep;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const bool hit = __shfl_sync(0xFFFFFFFFu, key[i], my_lane) == my_key;
+    if (hit && seen == 0) at = i;
+    seen -= hit;
+  }
+  int id = my_key != 0u ? (my_lane / sp.lanes) * size + (my_lane & (sp.lanes - 1)) * sp.per_lane + at : -1;
+  float lid = id >= 0 ? load_logit<kBf16>(row, id) : 0.0f;
+  if (prove) {
+    const float bid = id >= 0 ? __ldg(a.bias + id) : 0.0f;
+    uint32_t next = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
+    const float nl = __shfl_down_sync(0xFFFFFFFFu, lid, 1), nb = __shfl_down_sync(0xFFFFFFFFu, bid, 1);
+    bool twin = lid == nl && bid == nb;
+    const uint32_t rest = redux_max(s[0]);  // of 32 places, the last against the best expert left out
+    if (lane == 31) {
+      next = rest;
+      twin = false;
+    }
+    bool sure = true;
+    if (lane < a.top_k && my_key != 0u && next != 0u) {
+      const float v = value_of(my_key), n = value_of(next);
+      sure = twin || v - n > tol + 0x1p-22f * fmaxf(fabsf(v), fabsf(n));
+    }
+    certain = certain && __all_sync(0xFFFFFFFFu, sure);
+  }
+  if (!certain) {
+    id = route_choose_f64<kBf16>(a, row, route_keys + static_cast<int64_t>(warp) * a.E, row_max);
+    lid = id >= 0 ? load_logit<kBf16>(row, id) : 0.0f;
+  }
+  const bool found = id >= 0 && lane < a.top_k;
+  const float w = route_weight(lid, found, a.sigmoid, a.renorm, a.scale, row_max, row_sum);
+  if (lane < a.top_k) {
+    a.ids[t * a.top_k + lane] = id;
+    a.weights[t * a.top_k + lane] = w;
+  }
+}
+
+// Every row in binary64: for splits that leave a lane more experts than the
+// register kernel holds.
 template <bool kBf16>
-__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_f64_kernel(RouteArgs a) {
   extern __shared__ double route_keys[];  // [kRouteWarps][E]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;

@@ -309,12 +309,13 @@ FP8Q_API int fp8_gemm_unpromoted_diag(const uint8_t* qa, const float* sa, const 
  *   key     p + bias where a bias is given (a load-balancing bias moves the
  *           choice, not the weights), else p;
  *   groups  with n_group > 1 the E / n_group consecutive experts of a group
- *           share the sum of the group's best group_top (1 or 2) keys, and the
- *           topk_group groups with the largest sums stay;
+ *           share the group's best key (group_top = 1) or the sum of its best
+ *           two (group_top = 2), and the topk_group best groups stay;
  *   choice  the top_k largest keys among the experts that stay, largest first;
  *   weight  scale * p, or with renorm scale * p / (sum of the chosen p).
- * Keys are compared as binary64 values of these expressions; equal keys, and
- * equal groups, go to the lower index.  An expert whose logit or bias is -inf
+ * Keys and sums are compared as binary64 values of these expressions (single
+ * keys without a bias as the logits themselves, which have the same order);
+ * equal keys, and equal groups, go to the lower index.  An expert whose logit or bias is -inf
  * or NaN is never chosen; a place that finds no expert (a row whose mask leaves
  * fewer than top_k) gets id -1 and weight 0, and renorm runs over the others.
  * A logit of +inf counts as the largest finite float.

@@ -80,7 +80,9 @@ def route(logits, top_k, bias=None, score="softmax", n_group=1, topk_group=1, gr
         if n_group > 1:
             totals = []
             for g in range(n_group):
-                k = np.sort(key[t, g * size:(g + 1) * size])[::-1][:group_top]
+                # single keys without a bias compare as their logits (order)
+                by = key if group_top == 2 else order
+                k = np.sort(by[t, g * size:(g + 1) * size])[::-1][:group_top]
                 k = k[k > NEG]
                 totals.append(k.sum() if k.size else NEG)
             best = sorted(range(n_group), key=lambda g: (-totals[g], g))[:topk_group]
