@@ -780,26 +780,37 @@ int fp8_gemm_wgrad(const uint8_t* q_dy_t, const float* s_dy, const uint8_t* q_x_
 // most 32 / n_group, each lane an equal share of the group's experts, and the
 // instance is the least that holds the share.  Shares above 32 (over 16
 // groups, not a power of two, of over 32 experts) take the binary64 kernel.
+template <int VPL, bool kBf16>
+static void launch_route_vpl(const RouteArgs& a, const RouteSplit& sp, unsigned grid, size_t smem,
+                             cudaStream_t stream) {
+  if (a.sigmoid)
+    moe_route_kernel<VPL, kBf16, true><<<grid, 32 * kRouteWarps, smem, stream>>>(a, sp);
+  else
+    moe_route_kernel<VPL, kBf16, false><<<grid, 32 * kRouteWarps, smem, stream>>>(a, sp);
+}
+
 template <bool kBf16>
-static void launch_route(const RouteArgs& a, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((a.T + kRouteWarps - 1) / kRouteWarps);
-  const unsigned block = 32 * kRouteWarps;
+static void launch_route(const RouteArgs& a, int num_sms, cudaStream_t stream) {
+  const int64_t ctas = (a.T + kRouteWarps - 1) / kRouteWarps, cap = static_cast<int64_t>(num_sms) * kRouteCtasPerSm;
+  const unsigned grid = static_cast<unsigned>(ctas < cap ? ctas : cap);  // one wave: the warps walk the rows
   const size_t smem = static_cast<size_t>(kRouteWarps) * a.E * sizeof(double);
-  const int size = a.E / a.n_group;
-  RouteSplit sp{32, 0, 0};
-  while (sp.lanes * a.n_group > 32) sp.lanes /= 2;
-  sp.per_lane = (size + sp.lanes - 1) / sp.lanes;
+  RouteSplit sp{a.E / a.n_group, 5, 0, 0};
+  while (a.n_group << sp.lanes_log2 > 32) --sp.lanes_log2;
+  const int lanes = 1 << sp.lanes_log2;
+  sp.per_lane = (sp.size + lanes - 1) / lanes;
   int vpl = 1;
   while (vpl < sp.per_lane) vpl *= 2;
-  sp.vector = a.E == 32 * vpl && sp.lanes * sp.per_lane == size && aligned(a.logits, 16);
+  sp.vector = a.E == 32 * vpl && lanes * sp.per_lane == sp.size && aligned(a.logits, 16);
   switch (vpl) {
-    case 1: moe_route_kernel<1, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
-    case 2: moe_route_kernel<2, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
-    case 4: moe_route_kernel<4, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
-    case 8: moe_route_kernel<8, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
-    case 16: moe_route_kernel<16, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
-    case 32: moe_route_kernel<32, kBf16><<<grid, block, smem, stream>>>(a, sp); break;
-    default: moe_route_f64_kernel<kBf16><<<grid, block, smem, stream>>>(a);
+    case 1: launch_route_vpl<1, kBf16>(a, sp, grid, smem, stream); break;
+    case 2: launch_route_vpl<2, kBf16>(a, sp, grid, smem, stream); break;
+    case 4: launch_route_vpl<4, kBf16>(a, sp, grid, smem, stream); break;
+    case 8: launch_route_vpl<8, kBf16>(a, sp, grid, smem, stream); break;
+    case 16: launch_route_vpl<16, kBf16>(a, sp, grid, smem, stream); break;
+    case 32: launch_route_vpl<32, kBf16>(a, sp, grid, smem, stream); break;
+    default:
+      moe_route_f64_kernel<kBf16>
+          <<<static_cast<unsigned>(ctas), 32 * kRouteWarps, smem, stream>>>(a);
   }
 }
 
@@ -846,9 +857,9 @@ int fp8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t E, con
               static_cast<int32_t>(n_group), static_cast<int32_t>(topk_group), static_cast<int32_t>(group_top),
               sigmoid != 0, renorm != 0, scale};
   if (logits_bf16)
-    launch_route<true>(a, stream);
+    launch_route<true>(a, dev->num_sms, stream);
   else
-    launch_route<false>(a, stream);
+    launch_route<false>(a, dev->num_sms, stream);
   return launched();
 }
 

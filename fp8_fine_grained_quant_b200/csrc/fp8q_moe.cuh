@@ -85,26 +85,25 @@ __device__ __forceinline__ const void* logits_row(const void* logits, int64_t t,
 }
 
 // Weights of the chosen experts: lane j holds id (or -1) and returns its weight.
-// Sigmoid ratios are formed from e^(l - m) / (1 + e^l) with m = min(0, largest
-// chosen logit), which stays finite and nonzero when every chosen score
-// underflows.  row_max and row_sum are the softmax statistics of the whole row
-// (used without renorm).
+// Where a chosen sigmoid could underflow, its ratios are formed from
+// e^(l - c) / (1 + e^l) with c = min(0, largest chosen logit), which stays
+// finite and keeps the largest at 1/2 or more.  row_max and row_sum are the
+// softmax statistics of the whole row (used without renorm).
 __device__ __forceinline__ float route_weight(float l, bool found, bool sigmoid, bool renorm, float scale,
                                               float row_max, float row_sum) {
   float p;
-  if (renorm) {
-    const float m = warp_max(found ? l : neg_inf_f32());
-    if (sigmoid) {
-      const float c = fminf(m, 0.0f);
-      p = l > 0.0f ? 1.0f / (1.0f + expf(-l)) : expf(l - c) / (1.0f + expf(l));
-    } else {
-      p = expf(l - m);
+  if (sigmoid) {
+    p = div_full(1.0f, 1.0f + expf(-l));
+    if (renorm && __any_sync(0xFFFFFFFFu, found && l < -64.0f)) {
+      const float c = fminf(warp_max(found ? l : neg_inf_f32()), 0.0f);
+      p = l > 0.0f ? p : div_full(expf(l - c), 1.0f + expf(l));
     }
-    const float total = warp_sum(found ? p : 0.0f);
-    p /= total;
+  } else if (renorm) {
+    p = expf(l - warp_max(found ? l : neg_inf_f32()));
   } else {
-    p = sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - row_max) / row_sum;
+    p = div_full(expf(l - row_max), row_sum);
   }
+  if (renorm) p = div_full(p, warp_sum(found ? p : 0.0f));
   return found ? scale * p : 0.0f;
 }
 
@@ -229,23 +228,32 @@ __device__ __forceinline__ float rcp_approx(float v) {
   return r;
 }
 
+// e^x for comparisons: 2^(x log2 e) by ex2.approx.ftz (2 ulp), the product
+// rounded; off by at most (2 + |x|) 2^-23 relative.
+__device__ __forceinline__ float exp_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504f));
+  return r;
+}
+
 // How the experts of a row lie over a warp: the lanes of group g are
-// g * lanes .. + lanes - 1, each with `per_lane` consecutive experts of the
-// group, so lane order is expert order.  With one group: 32 lanes.
+// g << lanes_log2 and the next ones, each with `per_lane` consecutive experts
+// of the group, so lane order is expert order.  With one group: 32 lanes.
 struct RouteSplit {
-  int32_t lanes;     // of a group, a power of two
-  int32_t per_lane;  // at most the kernel's VPL
-  int32_t vector;    // the lanes' runs tile the row and are aligned: vector loads
+  int32_t size;        // experts of a group
+  int32_t lanes_log2;  // lanes of a group
+  int32_t per_lane;    // at most the kernel's VPL
+  int32_t vector;      // the lanes' runs tile the row and are aligned: vector loads
 };
 
-// A lane's logits l[i] (expert base + i), -inf past its share.
+// A lane's logits as loaded: with vector loads VPL consecutive values, else
+// one value a word (the type's -inf past the lane's share).
 template <int VPL, bool kBf16>
-__device__ __forceinline__ void load_share(const void* row, int base, int count, bool vector, float (&l)[VPL]) {
-  constexpr int kBytes = VPL * (kBf16 ? 2 : 4);
-  if (kBytes >= 4 && vector) {
-    constexpr int kWords = kBytes >= 4 ? kBytes / 4 : 1;
-    uint32_t w[kWords];
-    const uint8_t* p = static_cast<const uint8_t*>(row) + static_cast<int64_t>(base) * (kBf16 ? 2 : 4);
+__device__ __forceinline__ void load_share(const void* row, int base, int count, bool vector, uint32_t (&w)[VPL]) {
+  constexpr int kSize = kBf16 ? 2 : 4;
+  constexpr int kWords = VPL * kSize / 4;  // 0: too few for a word, never vector
+  if (kWords > 0 && vector) {
+    const uint8_t* p = static_cast<const uint8_t*>(row) + static_cast<int64_t>(base) * kSize;
     if constexpr (kWords >= 4) {
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
@@ -262,194 +270,214 @@ __device__ __forceinline__ void load_share(const void* row, int base, int count,
     } else {
       w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if constexpr (kBf16)
-        l[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
-      else
-        l[i] = __uint_as_float(w[i < kWords ? i : 0]);
-    }
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      l[i] = neg_inf_f32();
-      if (i < count) {
-        if constexpr (kBf16)
-          l[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(row)[base + i]);
-        else
-          l[i] = static_cast<const float*>(row)[base + i];
-      }
+      if constexpr (kBf16)
+        w[i] = i < count ? __ldg(static_cast<const uint16_t*>(row) + base + i) : 0xFF80u;
+      else
+        w[i] = i < count ? __ldg(static_cast<const uint32_t*>(row) + base + i) : 0xFF800000u;
     }
   }
+}
+template <int VPL, bool kBf16>
+__device__ __forceinline__ void share_values(const uint32_t (&w)[VPL], bool vector, float (&l)[VPL]) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) l[i] = l[i] > neg_inf_f32() ? fminf(l[i], FLT_MAX) : neg_inf_f32();
+  for (int i = 0; i < VPL; ++i) {
+    if constexpr (!kBf16)
+      l[i] = __uint_as_float(w[i]);
+    else if (VPL > 1 && vector)
+      l[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
+    else
+      l[i] = __uint_as_float(w[i] << 16);
+  }
 }
 
 constexpr int kRouteWarps = 4;
+constexpr int kRouteCtasPerSm = 8;  // up to eight experts a lane: 64 registers
 
 // The common case in FP32, with a proof: a warp holds its row in registers,
 // each lane its share's keys in descending order.  A round of the choice takes
 // the largest of the lanes' heads (one warp reduction); the lowest lane that
-// has it gives it up.
+// has it gives it up.  A warp walks rows at a stride of the grid, the next
+// row's logits loaded while it chooses from the current one.
 //
 // Without a bias experts are compared by their logits, exactly.  With one, and
 // for group sums, FP32 keys are compared, and each comparison that decides
 // (neighbours in the choice, the first expert left out, the worst group kept
 // against the best one dropped) must be wider than the keys' error; a row
 // where one is not goes to route_choose_f64.  Equal keys of equal logits and
-// biases need no proof.  The errors, with __expf off by (2 + 1.173 |x|) ulp:
-//   sigmoid  p (1 - p) (2 + 1.173 |x|) 2^-23 <= 2^-23, + 2^-23 (1 + e) and rcp:
-//            below 2^-21.6 a key; + 2^-24 |key| from adding the bias;
+// biases need no proof.  The errors, by exp_approx's:
+//   sigmoid  p (1 - p) (2 + |x|) 2^-23 <= 2^-23, + 2^-24 from 1 + e and 2^-23
+//            from rcp: below 2^-21.6 a key; + 2^-24 |key| from adding the bias;
 //   softmax  at most 30 * 2^-23 of p from the row's sum (37 additions, and
 //            sum p |x| <= ln 1024), and 3 * 2^-23: below 2^-17.9 for any two
 //            keys, as their p sum to at most 1;
 // so two keys further apart than 2^-20 (sigmoid) or 2^-17 (softmax) + 2^-22 of
 // the larger are in order; for sums of two keys, twice that.
-template <int VPL, bool kBf16>
-__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(RouteArgs a, RouteSplit sp) {
+template <int VPL, bool kBf16, bool kSigmoid>
+__global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm : 1) moe_route_kernel(RouteArgs a, RouteSplit sp) {
   extern __shared__ double route_keys[];  // [kRouteWarps][E]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-  if (t >= a.T) return;
-  const void* row = logits_row<kBf16>(a.logits, t, a.E);
-  const int size = a.E / a.n_group;
-  const int g = lane / sp.lanes;
-  const int first = (lane & (sp.lanes - 1)) * sp.per_lane;
-  const int base = g * size + first;
-  const int count = g < a.n_group ? max(0, min(sp.per_lane, size - first)) : 0;
-  float l[VPL];
-  load_share<VPL, kBf16>(row, base, count, sp.vector, l);
-
-  // softmax statistics of the row, where something needs them
+  const int g = lane >> sp.lanes_log2;
+  const int first = (lane & ((1 << sp.lanes_log2) - 1)) * sp.per_lane;
+  const int base = g * sp.size + first;
+  const int count = g < a.n_group ? max(0, min(sp.per_lane, sp.size - first)) : 0;
+  const bool biased = a.bias != nullptr;
   const bool pair_sums = a.n_group > 1 && a.group_top == 2;
-  float row_max = neg_inf_f32(), row_sum = 0.0f;
-  if (!a.sigmoid && (a.bias != nullptr || pair_sums || !a.renorm)) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) row_max = fmaxf(row_max, l[i]);
-    row_max = warp_max(row_max);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if (l[i] > neg_inf_f32()) row_sum += a.renorm ? __expf(l[i] - row_max) : expf(l[i] - row_max);
-    }
-    row_sum = warp_sum(row_sum);
-  }
-  const float inv_sum = rcp_approx(row_sum);
-  auto score = [&](float x) {
-    return a.sigmoid ? rcp_approx(1.0f + __expf(-x)) : __expf(x - row_max) * inv_sum;
-  };
-
-  // keys: the logits, or score + bias
-  uint32_t key[VPL], s[VPL];
-  if (a.bias == nullptr) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = l[i] > neg_inf_f32() ? key_of(l[i] + 0.0f) : 0u;  // -0 as +0
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const float b = i < count ? __ldg(a.bias + base + i) : 0.0f;
-      key[i] = l[i] > neg_inf_f32() && b > neg_inf_f32() ? key_of(score(l[i]) + b + 0.0f) : 0u;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) s[i] = key[i];
-  sort_descending<VPL>(s);
-
-  const float tol = a.sigmoid ? 0x1p-20f : 0x1p-17f;
-  bool certain = true;
-  if (a.n_group > 1) {
-    // the group's best one or two, in every lane of the group
-    uint32_t b1 = s[0], b2 = VPL > 1 ? s[VPL > 1 ? 1 : 0] : 0u;
-    for (int off = 1; off < sp.lanes; off <<= 1) {
-      const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, off), o2 = __shfl_xor_sync(0xFFFFFFFFu, b2, off);
-      b2 = max(min(b1, o1), max(b2, o2));
-      b1 = max(b1, o1);
-    }
-    uint32_t total = b1;  // group_top 1: the best key decides
-    const bool exact = a.group_top == 1 && a.bias == nullptr;
-    if (a.group_top == 2) {
-      float v1 = value_of(b1), v2 = value_of(b2);
-      if (a.bias == nullptr) {
-        v1 = score(v1);
-        v2 = score(v2);
-      }
-      total = b1 == 0u ? 0u : key_of(b2 == 0u ? v1 : v1 + v2);
-    }
-    int ahead = 0;
-    for (int h = 0; h < a.n_group; ++h) {
-      const uint32_t o = __shfl_sync(0xFFFFFFFFu, total, h * sp.lanes);
-      ahead += o > total || (o == total && h < g);
-    }
-    const bool in = g < a.n_group, keep = in && ahead < a.topk_group;
-    if (!exact && a.topk_group < a.n_group) {
-      const uint32_t worst = redux_min(keep ? total : 0xFFFFFFFFu), best = redux_max(in && !keep ? total : 0u);
-      const float w = value_of(worst), b = value_of(best);
-      certain = best == 0u || w - b > 2.0f * tol + 0x1p-20f * fmaxf(fabsf(w), fabsf(b));
-    }
-    if (!keep) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) s[i] = 0u;
-    }
-  }
-
-  // the choice: lane j gets place j's key, the lane that had it, and how many
-  // equal keys of that lane went before it
-  const bool prove = a.bias != nullptr;
-  const int rounds = a.top_k + (prove && a.top_k < 32 ? 1 : 0);
-  uint32_t my_key = 0u, last_key = 0u;
-  int my_lane = 0, my_rep = 0, last_lane = -1, rep = 0;
-  for (int j = 0; j < rounds; ++j) {
-    const uint32_t m = redux_max(s[0]);
-    if (m == 0u) break;
-    const int w = __ffs(__ballot_sync(0xFFFFFFFFu, s[0] == m)) - 1;
-    rep = m == last_key && w == last_lane ? rep + 1 : 0;
-    last_key = m;
-    last_lane = w;
-    if (lane == j) {
-      my_key = m;
-      my_lane = w;
-      my_rep = rep;
-    }
-    if (lane == w) {
-#pragma unroll
-      for (int i = 0; i + 1 < VPL; ++i) s[i] = s[i + 1];
-      s[VPL - 1] = 0u;
-    }
-  }
-  int at = 0, seen = my_rep;
+  const bool stats = !kSigmoid && (biased || pair_sums || !a.renorm);  // something needs the row's softmax
+  constexpr float tol = kSigmoid ? 0x1p-20f : 0x1p-17f;
+  float bias[VPL];  // -inf: never chosen
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const bool hit = __shfl_sync(0xFFFFFFFFu, key[i], my_lane) == my_key;
-    if (hit && seen == 0) at = i;
-    seen -= hit;
+    bias[i] = biased && i < count ? __ldg(a.bias + base + i) : 0.0f;
+    if (!(bias[i] > neg_inf_f32())) bias[i] = neg_inf_f32();
   }
-  int id = my_key != 0u ? (my_lane / sp.lanes) * size + (my_lane & (sp.lanes - 1)) * sp.per_lane + at : -1;
-  float lid = id >= 0 ? load_logit<kBf16>(row, id) : 0.0f;
-  if (prove) {
-    const float bid = id >= 0 ? __ldg(a.bias + id) : 0.0f;
-    uint32_t next = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
-    const float nl = __shfl_down_sync(0xFFFFFFFFu, lid, 1), nb = __shfl_down_sync(0xFFFFFFFFu, bid, 1);
-    bool twin = lid == nl && bid == nb;
-    const uint32_t rest = redux_max(s[0]);  // of 32 places, the last against the best expert left out
-    if (lane == 31) {
-      next = rest;
-      twin = false;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
+  uint32_t raw[VPL];
+  if (t < a.T) load_share<VPL, kBf16>(logits_row<kBf16>(a.logits, t, a.E), base, count, sp.vector, raw);
+  for (; t < a.T; t += step) {
+    const void* row = logits_row<kBf16>(a.logits, t, a.E);
+    float l[VPL];
+    share_values<VPL, kBf16>(raw, sp.vector, l);
+    if (t + step < a.T)
+      load_share<VPL, kBf16>(logits_row<kBf16>(a.logits, t + step, a.E), base, count, sp.vector, raw);
+    if (!kSigmoid || !biased) {  // a sigmoid of +inf needs no bound
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) l[i] = l[i] > neg_inf_f32() ? fminf(l[i], FLT_MAX) : neg_inf_f32();
     }
-    bool sure = true;
-    if (lane < a.top_k && my_key != 0u && next != 0u) {
-      const float v = value_of(my_key), n = value_of(next);
-      sure = twin || v - n > tol + 0x1p-22f * fmaxf(fabsf(v), fabsf(n));
+    float row_max = neg_inf_f32(), row_sum = 0.0f;
+    if (stats) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) row_max = fmaxf(row_max, l[i]);
+      row_max = warp_max(row_max);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (l[i] > neg_inf_f32()) row_sum += a.renorm ? exp_approx(l[i] - row_max) : expf(l[i] - row_max);
+      }
+      row_sum = warp_sum(row_sum);
     }
-    certain = certain && __all_sync(0xFFFFFFFFu, sure);
-  }
-  if (!certain) {
-    id = route_choose_f64<kBf16>(a, row, route_keys + static_cast<int64_t>(warp) * a.E, row_max);
-    lid = id >= 0 ? load_logit<kBf16>(row, id) : 0.0f;
-  }
-  const bool found = id >= 0 && lane < a.top_k;
-  const float w = route_weight(lid, found, a.sigmoid, a.renorm, a.scale, row_max, row_sum);
-  if (lane < a.top_k) {
-    a.ids[t * a.top_k + lane] = id;
-    a.weights[t * a.top_k + lane] = w;
+    const float inv_sum = rcp_approx(row_sum);
+    auto score = [&](float x) {
+      return kSigmoid ? rcp_approx(1.0f + exp_approx(-x)) : exp_approx(x - row_max) * inv_sum;
+    };
+
+    // keys: the logits (-0 as +0), or score + bias
+    uint32_t key[VPL], s[VPL];
+    if (!biased) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = l[i] > neg_inf_f32() ? key_of(l[i] + 0.0f) : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const float k = score(l[i]) + bias[i];
+        key[i] = l[i] > neg_inf_f32() && k > neg_inf_f32() ? key_of(k) : 0u;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s[i] = key[i];
+    sort_descending<VPL>(s);
+
+    bool certain = true;
+    if (a.n_group > 1) {
+      // the group's best one or two, in every lane of the group
+      uint32_t b1 = s[0], b2 = VPL > 1 ? s[VPL > 1 ? 1 : 0] : 0u;
+      for (int off = 1; off < (1 << sp.lanes_log2); off <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, off), o2 = __shfl_xor_sync(0xFFFFFFFFu, b2, off);
+        b2 = max(min(b1, o1), max(b2, o2));
+        b1 = max(b1, o1);
+      }
+      uint32_t total = b1;  // group_top 1: the best key decides
+      if (pair_sums) {
+        float v1 = value_of(b1), v2 = value_of(b2);
+        if (!biased) {
+          v1 = score(v1);
+          v2 = score(v2);
+        }
+        total = b1 == 0u ? 0u : key_of(b2 == 0u ? v1 : v1 + v2);
+      }
+      int ahead = 0;
+#pragma unroll 4
+      for (int h = 0; h < a.n_group; ++h) {
+        const uint32_t o = __shfl_sync(0xFFFFFFFFu, total, h << sp.lanes_log2);
+        ahead += o > total || (o == total && h < g);
+      }
+      const bool in = g < a.n_group, keep = in && ahead < a.topk_group;
+      if ((pair_sums || biased) && a.topk_group < a.n_group) {
+        const uint32_t worst = redux_min(keep ? total : 0xFFFFFFFFu), best = redux_max(in && !keep ? total : 0u);
+        const float w = value_of(worst), b = value_of(best);
+        certain = best == 0u || w - b > 2.0f * tol + 0x1p-20f * fmaxf(fabsf(w), fabsf(b));
+      }
+      if (!keep) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) s[i] = 0u;
+      }
+    }
+
+    // the choice: lane j gets place j's key and the lane that had it; with a
+    // bias also the first expert left out
+    const int rounds = a.top_k + (biased && a.top_k < 32 ? 1 : 0);
+    uint32_t my_key = 0u;
+    int my_lane = 0;
+    for (int j = 0; j < rounds; ++j) {
+      const uint32_t m = redux_max(s[0]);
+      const uint32_t have = __ballot_sync(0xFFFFFFFFu, s[0] == m);
+      if (m == 0u) break;
+      const int w = __ffs(have) - 1;
+      if (lane == j) {
+        my_key = m;
+        my_lane = w;
+      }
+      const bool mine = lane == w;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s[i] = mine ? (i + 1 < VPL ? s[i + 1 < VPL ? i + 1 : i] : 0u) : s[i];
+    }
+    // equal keys of one lane come one after another, in expert order: how many went before this one
+    const uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, my_key, 1);
+    const int prev_lane = __shfl_up_sync(0xFFFFFFFFu, my_lane, 1);
+    const uint32_t repeats =
+        __ballot_sync(0xFFFFFFFFu, lane > 0 && my_key != 0u && my_key == prev && my_lane == prev_lane);
+    int seen = 0;
+    if (repeats != 0u) seen = lane - (31 - __clz(~repeats & (0xFFFFFFFFu >> (31 - lane))));
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const bool hit = __shfl_sync(0xFFFFFFFFu, key[i], my_lane) == my_key;
+      if (hit && seen == 0) at = i;
+      seen -= hit;
+    }
+    int id = -1;
+    if (my_key != 0u)
+      id = (my_lane >> sp.lanes_log2) * sp.size + (my_lane & ((1 << sp.lanes_log2) - 1)) * sp.per_lane + at;
+    float lid = id >= 0 ? load_logit<kBf16>(row, id) : 0.0f;
+    if (biased) {
+      uint32_t next = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
+      const uint32_t rest = a.top_k == 32 ? redux_max(s[0]) : 0u;  // of 32 places, the first expert left out
+      if (lane == 31) next = rest;
+      bool sure = true;
+      if (lane < a.top_k && next != 0u) {
+        const float v = value_of(my_key), n = value_of(next);
+        sure = v - n > tol + 0x1p-22f * fmaxf(fabsf(v), fabsf(n));
+      }
+      if (!__all_sync(0xFFFFFFFFu, sure)) {
+        // keys in one another's reach: certain only between equal logits with equal biases
+        const float bid = id >= 0 ? __ldg(a.bias + id) : 0.0f;
+        const float nl = __shfl_down_sync(0xFFFFFFFFu, lid, 1), nb = __shfl_down_sync(0xFFFFFFFFu, bid, 1);
+        certain = certain && __all_sync(0xFFFFFFFFu, sure || (lane < 31 && lid == nl && bid == nb));
+      }
+    }
+    if (!certain) {
+      id = route_choose_f64<kBf16>(a, row, route_keys + static_cast<int64_t>(warp) * a.E, row_max);
+      lid = id >= 0 ? load_logit<kBf16>(row, id) : 0.0f;
+      __syncwarp();
+    }
+    const bool found = id >= 0 && lane < a.top_k;
+    const float w = route_weight(lid, found, kSigmoid, a.renorm, a.scale, row_max, row_sum);
+    if (lane < a.top_k) {
+      a.ids[t * a.top_k + lane] = id;
+      a.weights[t * a.top_k + lane] = w;
+    }
   }
 }
 
