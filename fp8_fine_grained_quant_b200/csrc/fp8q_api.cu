@@ -1038,17 +1038,17 @@ int fp8_swiglu_bwd_1x128(const void* dh_bf16, const uint8_t* qc, const float* sc
 int fp8_ckpt_128x1_t(const uint8_t* q, const float* s, int64_t M, int64_t K, int64_t Mp, uint8_t* qt, float* st,
                      cudaStream_t stream) {
   FP8Q_API_RANGE();
-  if (M < 0 || K < 0 || K % 128 || Mp < M || Mp % 128 || Mp >= kMaxRows || K >= kMaxRows) return FP8Q_ERR_SHAPE;
+  if (M < 0 || K < 0 || K % 128 || Mp < M || Mp % 128 || Mp >= kMaxRows || K >= kMaxRows ||
+      (Mp / 128) * (K / kCkptChannels) >= kMaxRows)  // one CTA each: the grid's x limit
+    return FP8Q_ERR_SHAPE;
   if (Mp == 0 || K == 0) return FP8Q_OK;
   if ((M && (!q || !s)) || !qt || !st) return FP8Q_ERR_NULL;
   if (!aligned(q, 16) || !aligned(s, 4) || !aligned(qt, 16) || !aligned(st, 16)) return FP8Q_ERR_ALIGN;
   DeviceInfo* dev = nullptr;
   int rc = device_info(&dev);
   if (rc) return rc;
-  const int64_t blocks = (Mp / 128) * (K / 128);
-  const int64_t cap = static_cast<int64_t>(dev->num_sms) * 24;
-  const int64_t grid = blocks < cap ? blocks : cap;
-  ckpt_128x1_t_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(q, s, qt, st, M, K, Mp, blocks);
+  const int64_t grid = (Mp / 128) * (K / kCkptChannels);
+  ckpt_128x1_t_kernel<<<static_cast<unsigned>(grid), 128, 0, stream>>>(q, s, qt, st, M, K, Mp);
   return launched();
 }
 

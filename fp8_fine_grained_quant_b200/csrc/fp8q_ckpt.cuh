@@ -20,8 +20,33 @@
 
 namespace fp8q {
 
-// Four E4M3 codes -> their values (exact).
-__device__ __forceinline__ void e4m3x4_to_f32(uint32_t c, float (&v)[4]) {
+// ------------------------------------------------------------ packed FP32
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t join_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split_f32x2(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Four E4M3 codes -> their values (exact), two packed pairs.
+__device__ __forceinline__ void e4m3x4_to_f32x2(uint32_t c, uint64_t& p0, uint64_t& p1) {
   uint32_t h0, h1;
   asm("{\n\t.reg .b16 a, b;\n\t"
       "mov.b32 {a, b}, %2;\n\t"
@@ -31,10 +56,78 @@ __device__ __forceinline__ void e4m3x4_to_f32(uint32_t c, float (&v)[4]) {
       : "r"(c));
   const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
   const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-  v[0] = f0.x;
-  v[1] = f0.y;
-  v[2] = f1.x;
-  v[3] = f1.y;
+  p0 = join_f32x2(f0.x, f0.y);
+  p1 = join_f32x2(f1.x, f1.y);
+}
+
+// ------------------------------------------------------------ codes by a corrected quotient
+// The code of fl32(x / s) without a division, a bracket or a branch: with
+// y = RN(1/s), q0 = x y, q1 = q0 + (x - q0 s) y.  Away from the E4M3 midpoints
+// q1 and fl32(x / s) are on the same side of each.  They could part only where
+// x / s is next to an FP32 rounding midpoint beside an E4M3 midpoint; there q0
+// is one of the two floats around it (x y is off by less than an ulp), x - q0 s
+// is exact, and what is left of y's error is below 2^-25 ulp, while x / s, a
+// quotient of two 24-bit numbers, is at least 2^-24 ulp away.  The same holds
+// for bf16 and for FP32 values x.  Needs y within half an ulp of 1/s, checked
+// exactly (1 - s y is a float), and s far from the ends of the range, so that no
+// remainder underflows where a code is decided; else the IEEE division.
+//
+// y is kept negated: with -q0 and -q1 a zero keeps its sign, and one XOR turns
+// four codes' signs back.  Three packed FP32 operations and one conversion a
+// pair of elements, against two products, two conversions and a comparison for
+// the bracket, and no element is ever redone.
+struct DivScale {
+  uint64_t ny2, s2;  // {-y, -y} and {s, s}
+  bool ok;
+};
+__device__ __forceinline__ bool corrected_reciprocal(float s, float& y) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  y = __fmaf_rn(r, __fmaf_rn(-s, r, 1.0f), r);
+  const float half_ulp = __uint_as_float(__float_as_uint(y) & 0x7F800000u) * 0x1p-24f;
+  return fabsf(__fmaf_rn(-s, y, 1.0f)) <= s * half_ulp && s >= 0x1p-80f && s <= 0x1p+120f;
+}
+__device__ __forceinline__ DivScale div_scale(float s) {
+  float y;
+  const bool ok = corrected_reciprocal(s, y);
+  return {pack_f32x2(-y), pack_f32x2(s), ok};
+}
+// -(x / s), corrected, for a pair.
+__device__ __forceinline__ uint64_t neg_quotient(uint64_t x, uint64_t ny2, uint64_t s2) {
+  const uint64_t q0 = mul_f32x2(x, ny2);
+  return fma_f32x2(fma_f32x2(q0, s2, x), ny2, q0);
+}
+__device__ __forceinline__ uint32_t codes4(uint64_t x0, uint64_t x1, const DivScale& d) {
+  return e4m3x4_from_f32x2(neg_quotient(x0, d.ny2, d.s2), neg_quotient(x1, d.ny2, d.s2)) ^ 0x80808080u;
+}
+// Codes of fl32(x / s) for four FP32 values by IEEE division.
+__device__ __noinline__ uint32_t codes4_exact(uint64_t x0, uint64_t x1, float s) {
+  float a, b, c, d;
+  split_f32x2(x0, a, b);
+  split_f32x2(x1, c, d);
+  return cvt_e4m3x2(__fdiv_rn(a, s), __fdiv_rn(b, s)) | (cvt_e4m3x2(__fdiv_rn(c, s), __fdiv_rn(d, s)) << 16);
+}
+// 16 bf16 (eight words) -> 16 codes, low byte first.
+__device__ __forceinline__ uint4 codes16_bf16(const uint32_t (&w)[8], float s) {
+  const DivScale d = div_scale(s);
+  if (!d.ok) return quantize16_exact(w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7], s);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = codes4(bf16x2_to_f32x2(w[2 * i]), bf16x2_to_f32x2(w[2 * i + 1]), d);
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+// 16 FP32 values (eight pairs) -> 16 codes.
+__device__ __forceinline__ uint4 codes16_f32(const uint64_t (&v)[8], float s) {
+  const DivScale d = div_scale(s);
+  uint32_t c[4];
+  if (d.ok) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = codes4(v[2 * i], v[2 * i + 1], d);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = codes4_exact(v[2 * i], v[2 * i + 1], s);
+  }
+  return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
 // s = fl32(amax / 448), 1 when that is 0, for any finite FP32 amax.
@@ -43,20 +136,79 @@ __device__ __forceinline__ float group_scale_f32(float amax) {
   return s == 0.0f ? 1.0f : s;
 }
 
-// E4M3 codes of fl32(x / s) for four FP32 values, by the bracket of 1/s where
-// it decides (see quantize16) and by IEEE division where it does not.
-__device__ __forceinline__ uint32_t quantize4_f32(const float (&x)[4], float s, float rlo, float rhi, bool exact_only) {
-  uint32_t lo = cvt_e4m3x2(__fmul_rn(x[0], rlo), __fmul_rn(x[1], rlo)) |
-                (cvt_e4m3x2(__fmul_rn(x[2], rlo), __fmul_rn(x[3], rlo)) << 16);
-  const uint32_t hi = cvt_e4m3x2(__fmul_rn(x[0], rhi), __fmul_rn(x[1], rhi)) |
-                      (cvt_e4m3x2(__fmul_rn(x[2], rhi), __fmul_rn(x[3], rhi)) << 16);
-  uint32_t m = exact_only ? 0x80808080u : nonzero_bytes(lo ^ hi);
-  for (; m != 0u; m &= m - 1u) {
-    const int j = (__ffs(m) - 1) >> 3;
-    const float v = j == 0 ? x[0] : (j == 1 ? x[1] : (j == 2 ? x[2] : x[3]));
-    lo = with_exact_code(lo, j, v, s);
+// ------------------------------------------------------------ exp(-g) for a pair
+// e^x = 2^(x L) with L = log2 e: t = fl(x L), and what t lacks, x L - t =
+// fma(x, L, -t) + x (log2 e - L), enters as a factor 1 + ln 2 times it.  With
+// ex2.approx (2^-22) the result is within 2^-21.9.  x = -g is held to
+// [-100, 88]: below, e^x counts for nothing beside 1; above, 1 / (1 + e^x) is 0
+// (flushed), which the callers treat as out of range.
+__device__ __forceinline__ uint64_t exp_neg_f32x2(uint64_t g2) {
+  float g0, g1;
+  split_f32x2(g2, g0, g1);
+  const uint64_t x = join_f32x2(fminf(fmaxf(-g0, -100.0f), 88.0f), fminf(fmaxf(-g1, -100.0f), 88.0f));
+  constexpr float kL = 1.44269504f;  // nearest FP32 to log2 e, 1.925963e-8 below it
+  const uint64_t nt = mul_f32x2(x, pack_f32x2(-kL));
+  uint64_t r = fma_f32x2(x, pack_f32x2(kL), nt);
+  r = fma_f32x2(x, pack_f32x2(1.925963e-8f), r);
+  float t0, t1, e0, e1;
+  split_f32x2(nt, t0, t1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(-t0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(-t1));
+  const uint64_t e = join_f32x2(e0, e1);
+  return fma_f32x2(e, mul_f32x2(r, pack_f32x2(0.693147181f)), e);
+}
+// 1 / (1 + e) by rcp.approx.ftz (1 ulp).
+__device__ __forceinline__ uint64_t rcp_one_plus(uint64_t e) {
+  float a, b, x, y;
+  split_f32x2(add_f32x2(e, pack_f32x2(1.0f)), a, b);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(a));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(b));
+  return join_f32x2(x, y);
+}
+
+// h = bf16(silu(g) u), correctly rounded, for the 16 elements of a lane; the
+// same values as swiglu16.  FP32: exp 2^-21.9 (weighted by 1 - p), 1 + e 2^-24,
+// rcp 2^-23, two products 2^-23: below 2^-20.8.  Where h (1 -+ 1.375 * 2^-21),
+// their roundings counted, give one bf16, that is it; elements they leave open
+// (about one in 3000), and those outside [2^-100, 2^120], are evaluated in
+// double, their words read again at gp and up.
+__device__ __forceinline__ void swiglu16_f32x2(const uint32_t (&gw)[8], const uint32_t (&uw)[8], uint32_t (&hw)[8],
+                                               const uint8_t* gp, const uint8_t* up) {
+  uint32_t d[8];
+  uint32_t any = 0u, most = 0u, least = 0x7F807F80u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t g = bf16x2_to_f32x2(gw[i]), u = bf16x2_to_f32x2(uw[i]);
+    const uint64_t h = mul_f32x2(mul_f32x2(g, rcp_one_plus(exp_neg_f32x2(g))), u);
+    hw[i] = bf16x2_from_pair(mul_f32x2(h, pack_f32x2(1.0f - 0x1.6p-21f)));
+    d[i] = hw[i] ^ bf16x2_from_pair(mul_f32x2(h, pack_f32x2(1.0f + 0x1.6p-21f)));
+    any |= d[i];
+    most = max_bf16x2(most, hw[i] & 0x7FFF7FFFu);
+    least = min_bf16x2(least, hw[i] & 0x7FFF7FFFu);
   }
-  return lo;
+  // bf16 bounds well inside the range where the error bound holds (NaN fails)
+  const bool in_range = max(most & 0xFFFFu, most >> 16) <= 0x7B00u && min(least & 0xFFFFu, least >> 16) >= 0x0E00u;
+  if (any == 0u && in_range) return;
+  uint32_t redo = 0u;  // bit 2i + j: half j of word i
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t m = (hw[i] >> (16 * j)) & 0x7FFFu;
+      // a zero factor makes an exact zero
+      const bool zero = ((gw[i] >> (16 * j)) & 0x7FFFu) == 0u || ((uw[i] >> (16 * j)) & 0x7FFFu) == 0u;
+      const bool open = ((d[i] >> (16 * j)) & 0xFFFFu) != 0u || ((m < 0x0E00u || m > 0x7B00u) && !zero);
+      redo |= static_cast<uint32_t>(open) << (2 * i + j);
+    }
+  }
+  for (; redo != 0u; redo &= redo - 1u) {
+    const int b = __ffs(redo) - 1, i = b >> 1, sh = (b & 1) * 16;
+    const uint32_t g = __ldg(reinterpret_cast<const uint32_t*>(gp) + i) >> sh << 16;
+    const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(up) + i) >> sh << 16;
+    const uint32_t x = swiglu_bf16_exact(__uint_as_float(g), __uint_as_float(u)) << sh;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) hw[k] = i == k ? (hw[k] & (0xFFFF0000u >> sh)) | x : hw[k];
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -85,7 +237,7 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_1x128_kernel(const uint8_t
     if (valid) {
       ld_nc_v8(c1 + gate * 2, gw);
       ld_nc_v8(c1 + (gate + inter) * 2, uw);
-      swiglu16(gw, uw, hw, c1 + gate * 2, c1 + (gate + inter) * 2);
+      swiglu16_f32x2(gw, uw, hw, c1 + gate * 2, c1 + (gate + inter) * 2);
     } else {
       zero8(gw);
       zero8(uw);
@@ -100,9 +252,9 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_1x128_kernel(const uint8_t
     }
     if (valid) {
       const float s_h = group_scale(ah), s_g = group_scale(ag), s_u = group_scale(au);
-      *reinterpret_cast<uint4*>(qh + t * 128 + sub * 16) = quantize16(hw, s_h, recip_pair(s_h), s_h < kMinFastScale);
-      *reinterpret_cast<uint4*>(qc + gate) = quantize16(gw, s_g, recip_pair(s_g), s_g < kMinFastScale);
-      *reinterpret_cast<uint4*>(qc + gate + inter) = quantize16(uw, s_u, recip_pair(s_u), s_u < kMinFastScale);
+      *reinterpret_cast<uint4*>(qh + t * 128 + sub * 16) = codes16_bf16(hw, s_h);
+      *reinterpret_cast<uint4*>(qc + gate) = codes16_bf16(gw, s_g);
+      *reinterpret_cast<uint4*>(qc + gate + inter) = codes16_bf16(uw, s_u);
       if (sub == 0) {
         sh[t] = s_h;
         const int64_t g = static_cast<int64_t>(row) * 2 * per_row + kb;
@@ -117,25 +269,58 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_1x128_kernel(const uint8_t
 // SwiGLU backward from the checkpoint.  With g = fl32(qc sc) of the gate half,
 // u of the up half and p = 1 / (1 + exp(-g)):
 //   d gate = dh u p (1 + g (1 - p)),   d up = dh g p
-// in FP32 (1 - p as exp(-g) p, which keeps its digits).  dc [rows, 2 inter] is
+// in FP32.  dc [rows, 2 inter] is
 // their bf16 rounding, for the weight gradient's token-axis quantizer; q and s
 // are their 1x128 tiles, the operand of the activation gradient's GEMM, taken
 // from the FP32 values: s = fl32(amax / 448), codes of fl32(d / s).
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void swiglu_bwd1(float g, float u, float dh, float& dg, float& du) {
-  const float e = expf(-g);
-  float p = div_full(1.0f, 1.0f + e);
-  // 1 - p = e / (1 + e); for g below -88 e overflows and p is 0
-  const float q = e > 0x1.fffffep+127f ? 1.0f : __fmul_rn(e, p);
-  du = dh * (g * p);
-  dg = dh * (u * (p * fmaf(g, q, 1.0f)));
+// Gradients of a pair: dg = dh (u (p (1 + g (1 - p)))), du = dh (g p).  With
+// E = exp(-|g|) and r = 1 / (1 + E), p and 1 - p are r and E r, the other way
+// round for negative gates: both keep their digits, and a p below FP32's normal
+// range is not flushed (E is the square of e^(-|g|/2), which stays normal: twice
+// ex2's error, E within 2^-20.9).  |g| beyond 104 makes E 0 either way.
+__device__ __forceinline__ void swiglu_bwd_f32x2(uint64_t g, uint64_t u, uint64_t dh, uint64_t& dg, uint64_t& du) {
+  float g0, g1;
+  split_f32x2(g, g0, g1);
+  const uint64_t x = join_f32x2(fminf(fabsf(g0), 104.0f), fminf(fabsf(g1), 104.0f));
+  // as in exp_neg_f32x2, for x / 2: L / 2, and what fl(x L / 2) lacks
+  constexpr float kHalfL = 0.72134752f;  // half of 1.44269504f
+  const uint64_t nt = mul_f32x2(x, pack_f32x2(-kHalfL));
+  uint64_t lack = fma_f32x2(x, pack_f32x2(kHalfL), nt);
+  lack = fma_f32x2(x, pack_f32x2(0.5f * 1.925963e-8f), lack);
+  float t0, t1, e0, e1;
+  split_f32x2(nt, t0, t1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
+  const uint64_t h = join_f32x2(e0, e1);
+  const uint64_t E = mul_f32x2(fma_f32x2(h, mul_f32x2(lack, pack_f32x2(-2.0f * 0.693147181f)), h), h);
+  const uint64_t r = rcp_one_plus(E), w = mul_f32x2(E, r);
+  float r0, r1, w0, w1;
+  split_f32x2(r, r0, r1);
+  split_f32x2(w, w0, w1);
+  const bool n0 = g0 < 0.0f, n1 = g1 < 0.0f;
+  const uint64_t p = join_f32x2(n0 ? w0 : r0, n1 ? w1 : r1), q = join_f32x2(n0 ? r0 : w0, n1 ? r1 : w1);
+  du = mul_f32x2(dh, mul_f32x2(g, p));
+  dg = mul_f32x2(dh, mul_f32x2(u, mul_f32x2(p, fma_f32x2(g, q, pack_f32x2(1.0f)))));
 }
 
-__global__ void __launch_bounds__(256) swiglu_bwd_1x128_kernel(const uint8_t* __restrict__ dh,
-                                                               const uint8_t* __restrict__ qc,
-                                                               const float* __restrict__ sc, uint8_t* __restrict__ dc,
-                                                               uint8_t* __restrict__ q, float* __restrict__ s,
-                                                               int64_t inter, int64_t num_tiles) {
+__device__ __forceinline__ float abs_max16_f32x2(const uint64_t (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float a, b;
+    split_f32x2(v[i], a, b);
+    m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+  }
+  return m;
+}
+
+__global__ void __launch_bounds__(256, 3) swiglu_bwd_1x128_kernel(const uint8_t* __restrict__ dh,
+                                                                  const uint8_t* __restrict__ qc,
+                                                                  const float* __restrict__ sc,
+                                                                  uint8_t* __restrict__ dc, uint8_t* __restrict__ q,
+                                                                  float* __restrict__ s, int64_t inter,
+                                                                  int64_t num_tiles) {
   const int sub = threadIdx.x & 7;
   const int64_t grp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
   const int64_t ngrp = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 3;
@@ -146,28 +331,25 @@ __global__ void __launch_bounds__(256) swiglu_bwd_1x128_kernel(const uint8_t* __
     const uint32_t kb = valid ? static_cast<uint32_t>(t) - row * per_row : 0u;
     const int64_t gate = static_cast<int64_t>(row) * 2 * inter + static_cast<int64_t>(kb) * 128 + sub * 16;
     const int64_t si = static_cast<int64_t>(row) * 2 * per_row + kb;
-    float dg[16], du[16];
+    uint64_t dg[8], du[8];
     float ag = 0.0f, au = 0.0f;
     if (valid) {
       uint32_t dw[8];
       ld_nc_v8(dh + t * 256 + sub * 32, dw);
       const uint4 cg = ld_nc_v4(qc + gate), cu = ld_nc_v4(qc + gate + inter);
       const uint32_t gc[4] = {cg.x, cg.y, cg.z, cg.w}, uc[4] = {cu.x, cu.y, cu.z, cu.w};
-      const float s_g = __ldg(sc + si), s_u = __ldg(sc + si + per_row);
+      const uint64_t s_g = pack_f32x2(__ldg(sc + si)), s_u = pack_f32x2(__ldg(sc + si + per_row));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float g[4], u[4];
-        e4m3x4_to_f32(gc[i], g);
-        e4m3x4_to_f32(uc[i], u);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w = dw[2 * i + (j >> 1)];
-          const float d = __uint_as_float((j & 1) ? (w & 0xFFFF0000u) : (w << 16));
-          swiglu_bwd1(__fmul_rn(g[j], s_g), __fmul_rn(u[j], s_u), d, dg[4 * i + j], du[4 * i + j]);
-          ag = fmaxf(ag, fabsf(dg[4 * i + j]));
-          au = fmaxf(au, fabsf(du[4 * i + j]));
-        }
+        uint64_t g0, g1, u0, u1;
+        e4m3x4_to_f32x2(gc[i], g0, g1);
+        e4m3x4_to_f32x2(uc[i], u0, u1);
+        swiglu_bwd_f32x2(mul_f32x2(g0, s_g), mul_f32x2(u0, s_u), bf16x2_to_f32x2(dw[2 * i]), dg[2 * i], du[2 * i]);
+        swiglu_bwd_f32x2(mul_f32x2(g1, s_g), mul_f32x2(u1, s_u), bf16x2_to_f32x2(dw[2 * i + 1]), dg[2 * i + 1],
+                         du[2 * i + 1]);
       }
+      ag = abs_max16_f32x2(dg);
+      au = abs_max16_f32x2(du);
     }
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) {
@@ -177,23 +359,15 @@ __global__ void __launch_bounds__(256) swiglu_bwd_1x128_kernel(const uint8_t* __
     if (!valid) continue;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const float(&d)[16] = half ? du : dg;
+      const uint64_t(&d)[8] = half ? du : dg;
       const float sv = group_scale_f32(half ? au : ag);
-      float rlo, rhi;
-      const bool ok = recip_bracket(sv, rlo, rhi);
-      const bool exact_only = !ok || sv < kMinFastScale;
-      uint32_t o[8], c[4];
+      uint32_t o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = bf16x2_rn(d[2 * i], d[2 * i + 1]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x[4] = {d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]};
-        c[i] = quantize4_f32(x, sv, rlo, rhi, exact_only);
-      }
+      for (int i = 0; i < 8; ++i) o[i] = bf16x2_from_pair(d[i]);
       const int64_t at = gate + half * inter;
       *reinterpret_cast<uint4*>(dc + at * 2) = make_uint4(o[0], o[1], o[2], o[3]);
       *reinterpret_cast<uint4*>(dc + at * 2 + 16) = make_uint4(o[4], o[5], o[6], o[7]);
-      *reinterpret_cast<uint4*>(q + at) = make_uint4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<uint4*>(q + at) = codes16_f32(d, sv);
       if (sub == 0) s[si + half * per_row] = sv;
     }
   }
@@ -206,95 +380,129 @@ __global__ void __launch_bounds__(256) swiglu_bwd_1x128_kernel(const uint8_t* __
 // v = fl32(code * s) are regrouped along tokens: st = fl32(amax / 448) (1 when
 // 0), codes E4M3(fl32(v / st)).
 //
-// A 256-thread CTA takes one 128-token x 128-channel block: thread t owns
-// channels 8 (t % 16) .. +7 of tokens 8 (t / 16) .. +7.  The per-channel
-// maxima are combined over the CTA, then every thread quantizes its 8 x 8
-// values; the code bytes are transposed in registers and through a swizzled
-// shared tile, and leave as full 128-byte rows.
+// A 128-thread CTA takes 128 tokens x 64 channels: thread t owns channels
+// 8 (t % 8) .. +7 of tokens 8 (t / 8) .. +7 and keeps their 64 values in
+// registers.  The per-channel maxima are combined over the CTA, one thread per
+// channel computes its scale and reciprocal, every thread quantizes its values
+// (codes by the corrected quotient, a scale a column), and the code bytes are
+// transposed in registers and through a swizzled shared tile, to leave as full
+// 128-byte rows.  Half a block of channels a CTA keeps five CTAs on an SM and
+// the last wave short.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256, 3) ckpt_128x1_t_kernel(const uint8_t* __restrict__ q,
+constexpr int kCkptChannels = 64;
+
+__global__ void __launch_bounds__(128, 5) ckpt_128x1_t_kernel(const uint8_t* __restrict__ q,
                                                               const float* __restrict__ s, uint8_t* __restrict__ qt,
-                                                              float* __restrict__ st, int64_t M, int64_t K, int64_t Mp,
-                                                              int64_t num_blocks) {
-  __shared__ __align__(16) uint8_t tile[128 * 128];
-  __shared__ __align__(16) float col_max[8][128];
-  __shared__ __align__(16) float ch_scale[128];
+                                                              float* __restrict__ st, int64_t M, int64_t K,
+                                                              int64_t Mp) {
+  __shared__ __align__(16) uint8_t tile[kCkptChannels * 128];
+  __shared__ __align__(16) float col_max[4][kCkptChannels];
+  __shared__ __align__(16) float ch_scale[kCkptChannels];
+  __shared__ __align__(16) float ch_ny[kCkptChannels];  // -1/s; NaN: the channel takes the division
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cg = tid & 15, rg = tid >> 4;
-  const int64_t nkc = K >> 7;
-  for (int64_t b = blockIdx.x; b < num_blocks; b += gridDim.x) {
-    const int64_t mb = b / nkc, kc = b - mb * nkc;
-    float v[8][8];  // [token][channel]
-    float m[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  const int cg = tid & 7, rg = tid >> 3;
+  const int64_t nkc = K / kCkptChannels;
+  const int64_t mb = static_cast<uint32_t>(blockIdx.x) / static_cast<uint32_t>(nkc);
+  const int64_t kc = static_cast<uint32_t>(blockIdx.x) - mb * nkc;
+  const int64_t tok0 = mb * 128 + rg * 8;
+  uint2 c[8];
+  float sr[8];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int64_t tok = mb * 128 + rg * 8 + r;
-      uint2 c = make_uint2(0u, 0u);
-      float sr = 1.0f;
-      if (tok < M) {
-        c = __ldg(reinterpret_cast<const uint2*>(q + tok * K + kc * 128 + cg * 8));
-        sr = __ldg(s + tok * nkc + kc);
-      }
-      float x[4];
-      e4m3x4_to_f32(c.x, x);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[r][i] = __fmul_rn(x[i], sr);
-      e4m3x4_to_f32(c.y, x);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[r][4 + i] = __fmul_rn(x[i], sr);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], fabsf(v[r][i]));
+  for (int r = 0; r < 8; ++r) {
+    c[r] = make_uint2(0u, 0u);
+    sr[r] = 1.0f;
+    if (tok0 + r < M) {
+      c[r] = __ldg(reinterpret_cast<const uint2*>(q + (tok0 + r) * K + kc * kCkptChannels + cg * 8));
+      sr[r] = __ldg(s + (tok0 + r) * (K >> 7) + (kc >> 1));
     }
-    // lanes l and l ^ 16 hold the same channels (two token groups of the warp)
+  }
+  uint64_t v[8][4];  // [token][channel pair]
+  float m[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 16));
-    if (lane < 16) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) col_max[warp][cg * 8 + i] = m[i];
-    }
-    __syncthreads();
-    if (tid < 128) {
-      float a = col_max[0][tid];
-#pragma unroll
-      for (int w = 1; w < 8; ++w) a = fmaxf(a, col_max[w][tid]);
-      const float sv = group_scale_f32(a);
-      ch_scale[tid] = sv;
-      st[mb * K + kc * 128 + tid] = sv;
-    }
-    __syncthreads();
-    uint32_t clo[8], chi[8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) clo[r] = chi[r] = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float sv = ch_scale[cg * 8 + i];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const uint32_t code = cvt_e4m3x2(__fdiv_rn(v[r][i], sv), 0.0f) & 0xFFu;
-        if (i < 4)
-          clo[r] |= code << (8 * i);
-        else
-          chi[r] |= code << (8 * (i - 4));
-      }
-    }
-    transpose8x8_bytes(clo, chi);  // now channel c: tokens 0-3 in clo[c], 4-7 in chi[c]
-    // channel row cg*8 + c of the tile, logical 8-byte slot rg, physical slot rg ^ cg
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-      *reinterpret_cast<uint2*>(tile + (cg * 8 + c) * 128 + ((rg ^ cg) << 3)) = make_uint2(clo[c], chi[c]);
-    __syncthreads();
-    uint8_t* dst = qt + (kc * 128) * Mp + mb * 128;
+  for (int r = 0; r < 8; ++r) {
+    const uint64_t s2 = pack_f32x2(sr[r]);
+    e4m3x4_to_f32x2(c[r].x, v[r][0], v[r][1]);
+    e4m3x4_to_f32x2(c[r].y, v[r][2], v[r][3]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int c = tid + 256 * i, row = c >> 3, ch = c & 7;
-      const int swz = row >> 3;
-      // logical slots 2ch, 2ch+1 sit in physical 16-byte chunk ch ^ (swz / 2),
-      // their halves swapped when swz is odd
-      uint4 o = *reinterpret_cast<const uint4*>(tile + row * 128 + ((ch ^ (swz >> 1)) << 4));
-      if (swz & 1) o = make_uint4(o.z, o.w, o.x, o.y);
-      *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(row) * Mp + ch * 16) = o;
+      v[r][i] = mul_f32x2(v[r][i], s2);
+      float a, b;
+      split_f32x2(v[r][i], a, b);
+      m[2 * i] = fmaxf(m[2 * i], fabsf(a));
+      m[2 * i + 1] = fmaxf(m[2 * i + 1], fabsf(b));
     }
-    __syncthreads();  // tile, col_max and ch_scale are reused
+  }
+  // lanes l, l ^ 8, l ^ 16 and l ^ 24 hold the same channels (the warp's four token groups)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 8));
+    m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 16));
+  }
+  if (lane < 8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<float4*>(&col_max[warp][cg * 8 + 4 * i]) =
+          make_float4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
+  }
+  __syncthreads();
+  if (tid < kCkptChannels) {
+    const float a = fmaxf(fmaxf(col_max[0][tid], col_max[1][tid]), fmaxf(col_max[2][tid], col_max[3][tid]));
+    const float sv = group_scale_f32(a);
+    float y;
+    const bool ok = corrected_reciprocal(sv, y);
+    ch_scale[tid] = sv;
+    ch_ny[tid] = ok ? -y : __int_as_float(0x7FC00000);
+    st[mb * K + kc * kCkptChannels + tid] = sv;
+  }
+  __syncthreads();
+  uint64_t ny2[4], s2[4];
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = *reinterpret_cast<const float2*>(&ch_ny[cg * 8 + 2 * i]);
+    const float2 x = *reinterpret_cast<const float2*>(&ch_scale[cg * 8 + 2 * i]);
+    ny2[i] = join_f32x2(y.x, y.y);
+    s2[i] = join_f32x2(x.x, x.y);
+    ok = ok && y.x < 0.0f && y.y < 0.0f;
+  }
+  uint32_t clo[8], chi[8];
+  if (ok) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      clo[r] = e4m3x4_from_f32x2(neg_quotient(v[r][0], ny2[0], s2[0]), neg_quotient(v[r][1], ny2[1], s2[1])) ^
+               0x80808080u;
+      chi[r] = e4m3x4_from_f32x2(neg_quotient(v[r][2], ny2[2], s2[2]), neg_quotient(v[r][3], ny2[3], s2[3])) ^
+               0x80808080u;
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      uint64_t d[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, b, x, y;
+        split_f32x2(v[r][i], a, b);
+        split_f32x2(s2[i], x, y);
+        d[i] = join_f32x2(__fdiv_rn(a, x), __fdiv_rn(b, y));
+      }
+      clo[r] = e4m3x4_from_f32x2(d[0], d[1]);
+      chi[r] = e4m3x4_from_f32x2(d[2], d[3]);
+    }
+  }
+  transpose8x8_bytes(clo, chi);  // now channel i: tokens 0-3 in clo[i], 4-7 in chi[i]
+  // channel row cg*8 + i of the tile, logical 8-byte slot rg, physical slot rg ^ 2cg: a
+  // half warp's sixteen stores fall in sixteen slots
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint2*>(tile + (cg * 8 + i) * 128 + ((rg ^ (2 * cg)) << 3)) = make_uint2(clo[i], chi[i]);
+  __syncthreads();
+  uint8_t* dst = qt + kc * kCkptChannels * Mp + mb * 128;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = (tid >> 3) + 16 * i, ch = tid & 7;
+    // logical slots 2ch and 2ch + 1 sit in physical 16-byte chunk ch ^ (row / 8)
+    *reinterpret_cast<uint4*>(dst + row * Mp + ch * 16) =
+        *reinterpret_cast<const uint4*>(tile + row * 128 + ((ch ^ (row >> 3)) << 4));
   }
 }
 
