@@ -198,7 +198,8 @@ _I32 = (torch.int32,)
 
 
 def _p(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return None if t is None else t.data_ptr()  # ctypes makes the pointer (argtypes)
+
 
 
 def _multiple(v: int, name: str):
@@ -651,27 +652,19 @@ def fp8_grouped_gemm_masked(qa, sa, qb, sb, masked_m, expected_m: int = 0, out: 
     return out
 
 
-# ---------------------------------------------------------------- mixture of experts
-MAX_EXPERTS = 1024
-MAX_TOP_K = 32
-MAX_GROUPS = 32
-_LOGITS = (torch.float32, torch.bfloat16)
+# ---------------------------------------------------------------- mixture of experts, 8-bit checkpoints
+# These calls are marshalled in C++ (csrc/fp8q_torch.cpp): the same checks and messages, a third of the time.
+_marshal = None
 
 
-def _score(score: str) -> int:
-    if score not in ("softmax", "sigmoid"):
-        raise ValueError("score must be 'softmax' or 'sigmoid', got %r" % (score,))
-    return int(score == "sigmoid")
-
-
-def _router(logits, top_k: int):
-    _tensor(logits, "logits", _LOGITS, (2,))
-    T, E = logits.shape
-    if not 1 <= E <= MAX_EXPERTS:
-        raise ValueError("logits have %d experts, 1 to %d are supported" % (E, MAX_EXPERTS))
-    if not 1 <= top_k <= min(E, MAX_TOP_K):
-        raise ValueError("top_k = %d is not in 1..%d" % (top_k, min(E, MAX_TOP_K)))
-    return T, E
+def _native():
+    """The marshalling module (raises if it has not been built)."""
+    global _marshal
+    if _marshal is None:
+        lib()  # its own message if nothing has been built
+        from . import _calls
+        _marshal = _calls
+    return _marshal
 
 
 def fp8_moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None, score: str = "softmax",
@@ -683,57 +676,15 @@ def fp8_moe_route(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = 
     ``n_group`` > 1 the ``topk_group`` groups with the largest sum of their best ``group_top`` (1 or 2) keys stay.
     ``renorm`` divides the chosen scores by their sum; ``scale`` multiplies the weights.  Ties go to the lower
     index; experts with a logit of -inf or NaN are never chosen, places without an expert get id -1, weight 0."""
-    top_k, n_group, topk_group, group_top = int(top_k), int(n_group), int(topk_group), int(group_top)
-    T, E = _router(logits, top_k)
-    sig = _score(score)
-    if not 1 <= n_group <= MAX_GROUPS or E % n_group:
-        raise ValueError("n_group = %d does not divide %d experts, or is not in 1..%d" % (n_group, E, MAX_GROUPS))
-    if not 1 <= topk_group <= n_group:
-        raise ValueError("topk_group = %d is not in 1..%d" % (topk_group, n_group))
-    if group_top not in (1, 2):
-        raise ValueError("group_top = %d is not 1 or 2" % group_top)
-    if top_k > topk_group * (E // n_group):
-        raise ValueError("top_k = %d exceeds the %d experts of %d groups" % (top_k, topk_group * (E // n_group),
-                                                                            topk_group))
-    _tensor(bias, "bias", _F32)
-    _tensor(ids, "ids", _I32)
-    _tensor(weights, "weights", _F32)
-    _numel(bias, E, "bias")
-    _numel(ids, T * top_k, "ids")
-    _numel(weights, T * top_k, "weights")
-    dev = _device_of(logits=logits, bias=bias, ids=ids, weights=weights)
-    if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check(lib().fp8_moe_route(_p(logits), logits.dtype == torch.bfloat16, T, E, _p(bias), sig, top_k, n_group,
-                                   topk_group, group_top, bool(renorm), float(scale), _p(ids), _p(weights),
-                                   _stream(stream, dev)), "fp8_moe_route")
-    return ids, weights
+    return _native().route(logits, top_k, bias, score, n_group, topk_group, group_top, renorm, scale, ids, weights,
+                          stream)
 
 
 def fp8_moe_route_bwd(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, score: str = "softmax",
                       renorm: bool = True, scale: float = 1.0, dlogits: torch.Tensor | None = None, stream=None):
     """Gradient of :func:`fp8_moe_route`'s weights: (logits [T,E], its ids [T,k], dweights [T,k] f32) ->
     dlogits [T,E] of the logits' type (the choice held constant; the bias has no gradient)."""
-    _tensor(ids, "ids", _I32, (2,))
-    top_k = ids.shape[1]
-    T, E = _router(logits, top_k)
-    sig = _score(score)
-    _tensor(dweights, "dweights", _F32)
-    _tensor(dlogits, "dlogits", (logits.dtype,))
-    _numel(ids, T * top_k, "ids")
-    _numel(dweights, T * top_k, "dweights")
-    _numel(dlogits, T * E, "dlogits")
-    dev = _device_of(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
-    if dlogits is None:
-        dlogits = torch.empty_like(logits)
-    with _on(dev):
-        _check(lib().fp8_moe_route_bwd(_p(logits), logits.dtype == torch.bfloat16, T, E, _p(ids), _p(dweights), sig,
-                                       top_k, bool(renorm), float(scale), _p(dlogits), _stream(stream, dev)),
-               "fp8_moe_route_bwd")
-    return dlogits
+    return _native().route_bwd(logits, ids, dweights, score, renorm, scale, dlogits, stream)
 
 
 def moe_contiguous_blocks(T: int, top_k: int, E: int) -> int:
@@ -743,88 +694,19 @@ def moe_contiguous_blocks(T: int, top_k: int, E: int) -> int:
     return (n + (TILE - 1) * min(n, E)) // TILE
 
 
-def _layout_ids(ids, E: int):
-    _tensor(ids, "ids", _I32, (2,))
-    T, top_k = ids.shape
-    if not 1 <= E <= MAX_EXPERTS:
-        raise ValueError("E = %d is not in 1..%d" % (E, MAX_EXPERTS))
-    if not 1 <= top_k <= MAX_TOP_K:
-        raise ValueError("ids have %d columns, 1 to %d are supported" % (top_k, MAX_TOP_K))
-    return T, top_k
-
-
 def fp8_moe_layout_contiguous(ids: torch.Tensor, E: int, slots: torch.Tensor | None = None,
                               m_indices: torch.Tensor | None = None, counts: torch.Tensor | None = None, stream=None):
     """Contiguous layout of chosen experts ids [T,k] int32: (slots [T,k], m_indices [B], counts [E]) int32 with
     B = :func:`moe_contiguous_blocks`.  Entry order within an expert; entries without an expert get slot -1,
     blocks past the last m_indices -1 (skipped by the grouped GEMM)."""
-    E = int(E)
-    T, top_k = _layout_ids(ids, E)
-    B = moe_contiguous_blocks(T, top_k, E)
-    for t, name in ((slots, "slots"), (m_indices, "m_indices"), (counts, "counts")):
-        _tensor(t, name, _I32)
-    _numel(slots, T * top_k, "slots")
-    _numel(m_indices, B, "m_indices")
-    _numel(counts, E, "counts")
-    dev = _device_of(ids=ids, slots=slots, m_indices=m_indices, counts=counts)
-    if slots is None:
-        slots = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    if m_indices is None:
-        m_indices = torch.empty((B,), dtype=torch.int32, device=dev)
-    if counts is None:
-        counts = torch.empty((E,), dtype=torch.int32, device=dev)
-    with _on(dev):
-        _check(lib().fp8_moe_layout_contiguous(_p(ids), T, top_k, E, _p(slots), _p(m_indices), _p(counts),
-                                               _stream(stream, dev)), "fp8_moe_layout_contiguous")
-    return slots, m_indices, counts
+    return _native().layout_contiguous(ids, E, slots, m_indices, counts, stream)
 
 
 def fp8_moe_layout_masked(ids: torch.Tensor, E: int, cap: int, slots: torch.Tensor | None = None,
                           masked_m: torch.Tensor | None = None, stream=None):
     """Masked layout of chosen experts ids [T,k] int32: (slots [T,k], masked_m [E]) int32.  Slot expert * cap +
     rank; entries past an expert's capacity, or without an expert, get -1."""
-    E, cap = int(E), int(cap)
-    T, top_k = _layout_ids(ids, E)
-    if cap < TILE:
-        raise ValueError("cap = %d is below %d" % (cap, TILE))
-    _multiple(cap, "cap")
-    _tensor(slots, "slots", _I32)
-    _tensor(masked_m, "masked_m", _I32)
-    _numel(slots, T * top_k, "slots")
-    _numel(masked_m, E, "masked_m")
-    dev = _device_of(ids=ids, slots=slots, masked_m=masked_m)
-    if slots is None:
-        slots = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    if masked_m is None:
-        masked_m = torch.empty((E,), dtype=torch.int32, device=dev)
-    with _on(dev):
-        _check(lib().fp8_moe_layout_masked(_p(ids), T, top_k, E, cap, _p(slots), _p(masked_m), _stream(stream, dev)),
-               "fp8_moe_layout_masked")
-    return slots, masked_m
-
-
-def _slots(slots, T: int):
-    _tensor(slots, "slots", _I32, (2,))
-    if slots.shape[0] != T:
-        raise ValueError("slots are for %d tokens, the call has %d" % (slots.shape[0], T))
-    if not 1 <= slots.shape[1] <= MAX_TOP_K:
-        raise ValueError("slots have %d columns, 1 to %d are supported" % (slots.shape[1], MAX_TOP_K))
-    return slots.shape[1]
-
-
-def _pad_layout(m_indices, counts, rows: int) -> int:
-    """The contiguous layout's arrays (both or neither); returns the expert count."""
-    _tensor(m_indices, "m_indices", _I32)
-    _tensor(counts, "counts", _I32)
-    if (m_indices is None) != (counts is None):
-        raise ValueError("m_indices and counts go together")
-    if m_indices is None:
-        return 0
-    _multiple(rows, "rows")
-    _numel(m_indices, rows // TILE, "m_indices")
-    if not 1 <= counts.numel() <= MAX_EXPERTS:
-        raise ValueError("counts hold %d experts, 1 to %d are supported" % (counts.numel(), MAX_EXPERTS))
-    return counts.numel()
+    return _native().layout_masked(ids, E, cap, slots, masked_m, stream)
 
 
 def fp8_moe_dispatch_1x128(x: torch.Tensor, slots: torch.Tensor, rows: int, m_indices: torch.Tensor | None = None,
@@ -833,57 +715,14 @@ def fp8_moe_dispatch_1x128(x: torch.Tensor, slots: torch.Tensor, rows: int, m_in
     """Tokens x [T,D] bf16, 1x128-quantized once each, into the rows of their slots [T,k]: returns (q [rows,D]
     float8_e4m3fn, s [rows,D/128] f32).  With the contiguous layout's m_indices and counts, the rows that pad an
     expert's last block get codes 0 and scale 1.  Other rows are left as they were: pass q and s to keep them."""
-    _tensor(x, "x", _BF16, (2,))
-    T, D = x.shape
-    _multiple(D, "D")
-    rows = int(rows)
-    if rows < 0:
-        raise ValueError("rows = %d is negative" % rows)
-    top_k = _slots(slots, T)
-    E = _pad_layout(m_indices, counts, rows)
-    _tensor(q, "q", _FP8)
-    _tensor(s, "s", _F32)
-    _numel(q, rows * D, "q")
-    _numel(s, rows * (D // TILE), "s")
-    dev = _device_of(x=x, slots=slots, m_indices=m_indices, counts=counts, q=q, s=s)
-    if q is None:
-        q = torch.empty((rows, D), dtype=torch.float8_e4m3fn, device=dev)
-    if s is None:
-        s = torch.empty((rows, D // TILE), dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check(lib().fp8_moe_dispatch_1x128(_p(x), T, D, _p(slots), top_k, rows, _p(m_indices), _p(counts), E, _p(q),
-                                            _p(s), _stream(stream, dev)), "fp8_moe_dispatch_1x128")
-    return q, s
-
-
-def _expert_rows(y, name: str):
-    """Expert outputs [rows,D] or [E,cap,D] bf16: their row count and width."""
-    _tensor(y, name, _BF16, (2, 3))
-    D = y.shape[-1]
-    _multiple(D, "D")
-    rows = y.shape[0] if y.dim() == 2 else y.shape[0] * y.shape[1]
-    return rows, D
+    return _native().dispatch_1x128(x, slots, rows, m_indices, counts, q, s, stream)
 
 
 def fp8_moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None,
                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """out [T,D] bf16 = sum over j of weights[t,j] * y[slots[t,j]] for y [rows,D] or [E,cap,D] bf16.  Without
     weights the plain sum: the gradient of :func:`fp8_moe_dispatch_1x128`'s tokens from its rows' gradients."""
-    rows, D = _expert_rows(y, "y")
-    _tensor(slots, "slots", _I32, (2,))
-    T = slots.shape[0]
-    top_k = _slots(slots, T)
-    _tensor(weights, "weights", _F32)
-    _tensor(out, "out", _BF16)
-    _numel(weights, T * top_k, "weights")
-    _numel(out, T * D, "out")
-    dev = _device_of(y=y, slots=slots, weights=weights, out=out)
-    if out is None:
-        out = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
-    with _on(dev):
-        _check(lib().fp8_moe_combine(_p(y), rows, D, _p(slots), _p(weights), T, top_k, _p(out),
-                                     _stream(stream, dev)), "fp8_moe_combine")
-    return out
+    return _native().combine(y, slots, weights, out, stream)
 
 
 def fp8_moe_combine_bwd(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor,
@@ -892,66 +731,15 @@ def fp8_moe_combine_bwd(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tensor
     """Gradient of :func:`fp8_moe_combine`: dout [T,D] bf16 -> (dy, the shape of y, bf16; dweights [T,k] f32).
     Row slots[t,j] of dy gets weights[t,j] * dout[t]; with the contiguous layout's m_indices and counts the pad
     rows get zeros; other rows are left as they were: pass dy to keep them."""
-    rows, D = _expert_rows(y, "y")
-    _tensor(dout, "dout", _BF16, (2,))
-    T = dout.shape[0]
-    if dout.shape[1] != D:
-        raise ValueError("dout and y differ in D (%d, %d)" % (dout.shape[1], D))
-    top_k = _slots(slots, T)
-    if weights is None:
-        raise TypeError("weights must be a torch.Tensor")
-    _tensor(weights, "weights", _F32)
-    E = _pad_layout(m_indices, counts, rows)
-    _tensor(dy, "dy", _BF16)
-    _tensor(dweights, "dweights", _F32)
-    _numel(weights, T * top_k, "weights")
-    _numel(dy, rows * D, "dy")
-    _numel(dweights, T * top_k, "dweights")
-    dev = _device_of(dout=dout, y=y, slots=slots, weights=weights, m_indices=m_indices, counts=counts, dy=dy,
-                     dweights=dweights)
-    if dy is None:
-        dy = torch.empty_like(y)
-    elif dy.numel() and dy.data_ptr() == y.data_ptr():
-        raise ValueError("dy may not be y: its rows are read while dy is written")
-    if dweights is None:
-        dweights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check(lib().fp8_moe_combine_bwd(_p(dout), _p(y), rows, D, _p(slots), _p(weights), T, top_k, _p(m_indices),
-                                         _p(counts), E, _p(dy), _p(dweights), _stream(stream, dev)),
-               "fp8_moe_combine_bwd")
-    return dy, dweights
+    return _native().combine_bwd(dout, y, slots, weights, m_indices, counts, dy, dweights, stream)
 
 
-# ---------------------------------------------------------------- 8-bit activation checkpoints
 def fp8_swiglu_ckpt_1x128(c1: torch.Tensor, qh: torch.Tensor | None = None, sh: torch.Tensor | None = None,
                           qc: torch.Tensor | None = None, sc: torch.Tensor | None = None, stream=None):
     """SwiGLU with its 8-bit checkpoint: c1 [rows,2I] bf16 ([gate | up]) -> ((qh [rows,I], sh [rows,I/128]),
     (qc [rows,2I], sc [rows,2I/128])): what :func:`fp8_swiglu_quant_1x128` and :func:`fp8_quant_act_1x128` of c1
     return, in one pass.  (qc, sc) is all that :func:`fp8_swiglu_bwd_1x128` needs."""
-    _tensor(c1, "c1", _BF16, (2,))
-    rows = c1.shape[0]
-    if c1.shape[1] % (2 * TILE):
-        raise ValueError("c1's last dim %d is not 2 x a multiple of %d" % (c1.shape[1], TILE))
-    inter = c1.shape[1] // 2
-    for t, name, dt in ((qh, "qh", _FP8), (sh, "sh", _F32), (qc, "qc", _FP8), (sc, "sc", _F32)):
-        _tensor(t, name, dt)
-    _numel(qh, rows * inter, "qh")
-    _numel(sh, rows * (inter // TILE), "sh")
-    _numel(qc, rows * 2 * inter, "qc")
-    _numel(sc, rows * 2 * (inter // TILE), "sc")
-    dev = _device_of(c1=c1, qh=qh, sh=sh, qc=qc, sc=sc)
-    if qh is None:
-        qh = torch.empty((rows, inter), dtype=torch.float8_e4m3fn, device=dev)
-    if sh is None:
-        sh = torch.empty((rows, inter // TILE), dtype=torch.float32, device=dev)
-    if qc is None:
-        qc = torch.empty((rows, 2 * inter), dtype=torch.float8_e4m3fn, device=dev)
-    if sc is None:
-        sc = torch.empty((rows, 2 * (inter // TILE)), dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check(lib().fp8_swiglu_ckpt_1x128(_p(c1), rows, inter, _p(qh), _p(sh), _p(qc), _p(sc),
-                                           _stream(stream, dev)), "fp8_swiglu_ckpt_1x128")
-    return (qh, sh), (qc, sc)
+    return _native().swiglu_ckpt(c1, qh, sh, qc, sc, stream)
 
 
 def fp8_swiglu_bwd_1x128(dh: torch.Tensor, qc: torch.Tensor, sc: torch.Tensor, dc: torch.Tensor | None = None,
@@ -959,35 +747,7 @@ def fp8_swiglu_bwd_1x128(dh: torch.Tensor, qc: torch.Tensor, sc: torch.Tensor, d
     """SwiGLU backward from the checkpoint (qc [rows,2I], sc [rows,2I/128]): dh [rows,I] bf16 -> (dc [rows,2I]
     bf16, (q [rows,2I] float8_e4m3fn, s [rows,2I/128] f32)), the gradient of c1 and its 1x128 quantization
     (taken from the FP32 gradient, before its rounding to bf16)."""
-    _tensor(dh, "dh", _BF16, (2,))
-    _tensor(qc, "qc", _FP8, (2,))
-    _tensor(sc, "sc", _F32)
-    rows, inter = dh.shape
-    _multiple(inter, "inter")
-    if tuple(qc.shape) != (rows, 2 * inter):
-        raise ValueError("qc is %s, dh [%d, %d] needs [%d, %d]" % (tuple(qc.shape), rows, inter, rows, 2 * inter))
-    ns = rows * 2 * (inter // TILE)
-    _tensor(dc, "dc", _BF16)
-    _tensor(q, "q", _FP8)
-    _tensor(s, "s", _F32)
-    _numel(sc, ns, "sc")
-    _numel(dc, rows * 2 * inter, "dc")
-    _numel(q, rows * 2 * inter, "q")
-    _numel(s, ns, "s")
-    dev = _device_of(dh=dh, qc=qc, sc=sc, dc=dc, q=q, s=s)
-    for t, src, name in ((q, qc, "q may not be qc"), (s, sc, "s may not be sc")):
-        if t is not None and t.numel() and t.data_ptr() == src.data_ptr():
-            raise ValueError(name + ": the checkpoint is read while it is written")
-    if dc is None:
-        dc = torch.empty((rows, 2 * inter), dtype=torch.bfloat16, device=dev)
-    if q is None:
-        q = torch.empty((rows, 2 * inter), dtype=torch.float8_e4m3fn, device=dev)
-    if s is None:
-        s = torch.empty((rows, 2 * (inter // TILE)), dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check(lib().fp8_swiglu_bwd_1x128(_p(dh), _p(qc), _p(sc), rows, inter, _p(dc), _p(q), _p(s),
-                                          _stream(stream, dev)), "fp8_swiglu_bwd_1x128")
-    return dc, (q, s)
+    return _native().swiglu_bwd(dh, qc, sc, dc, q, s, stream)
 
 
 def fp8_ckpt_128x1_t(q: torch.Tensor, s: torch.Tensor, Mp: int | None = None, qt: torch.Tensor | None = None,
@@ -995,29 +755,7 @@ def fp8_ckpt_128x1_t(q: torch.Tensor, s: torch.Tensor, Mp: int | None = None, qt
     """The operand of :func:`fp8_gemm_wgrad` from an activation saved as 1x128 tiles (q [M,K], s [M,K/128]):
     (qt [K,Mp] float8_e4m3fn, st [Mp/128,K] f32), regrouped along tokens as :func:`fp8_quant_act_128x1_t` lays
     them out.  Mp defaults to M rounded up to 512; padding tokens get code 0."""
-    _tensor(q, "q", _FP8, (2,))
-    _tensor(s, "s", _F32)
-    M, K = q.shape
-    _multiple(K, "K")
-    _numel(s, M * (K // TILE), "s")
-    if Mp is None:
-        Mp = -(-M // WGRAD_TOKEN_GROUP) * WGRAD_TOKEN_GROUP
-    _multiple(Mp, "Mp")
-    if Mp < M:
-        raise ValueError("Mp = %d is below the token count %d" % (Mp, M))
-    _tensor(qt, "qt", _FP8)
-    _tensor(st, "st", _F32)
-    _numel(qt, K * Mp, "qt")
-    _numel(st, (Mp // TILE) * K, "st")
-    dev = _device_of(q=q, s=s, qt=qt, st=st)
-    if qt is None:
-        qt = torch.empty((K, Mp), dtype=torch.float8_e4m3fn, device=dev)
-    if st is None:
-        st = torch.empty((Mp // TILE, K), dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check(lib().fp8_ckpt_128x1_t(_p(q), _p(s), M, K, Mp, _p(qt), _p(st), _stream(stream, dev)),
-               "fp8_ckpt_128x1_t")
-    return qt, st
+    return _native().ckpt_128x1_t(q, s, Mp, qt, st, stream)
 
 
 def get_device_error(stream=None, device=None) -> int:
