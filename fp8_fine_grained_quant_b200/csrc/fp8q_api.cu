@@ -136,6 +136,9 @@ int device_info(DeviceInfo** out) {
                                    MxSmem::kDynamicBytes);
         if (e == cudaSuccess) e = opt_in_token_axis_smem<false>();
         if (e == cudaSuccess) e = opt_in_token_axis_smem<true>();
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(moe_layout_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   layout_smem(kMaxExperts));
         if (e != cudaSuccess) return FP8Q_ERR_CUDA;
       }
       d.ready.store(true, std::memory_order_release);
@@ -814,6 +817,26 @@ static void launch_route(const RouteArgs& a, int num_sms, cudaStream_t stream) {
   }
 }
 
+template <int VPL, bool kBf16>
+static void launch_route_bwd_vpl(const RouteBwdArgs& a, int num_sms, cudaStream_t stream) {
+  const int64_t ctas = (a.T + kRouteWarps - 1) / kRouteWarps, cap = static_cast<int64_t>(num_sms) * 16;
+  const unsigned grid = static_cast<unsigned>(ctas < cap ? ctas : cap);
+  const size_t smem = static_cast<size_t>(kRouteWarps) * a.E * sizeof(float);
+  if (!a.sigmoid && !a.renorm)
+    moe_route_bwd_kernel<VPL, kBf16, true><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
+  else
+    moe_route_bwd_kernel<VPL, kBf16, false><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
+}
+template <bool kBf16>
+static void launch_route_bwd(const RouteBwdArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.E <= 64)
+    launch_route_bwd_vpl<2, kBf16>(a, num_sms, stream);
+  else if (a.E <= 256)
+    launch_route_bwd_vpl<8, kBf16>(a, num_sms, stream);
+  else
+    launch_route_bwd_vpl<32, kBf16>(a, num_sms, stream);
+}
+
 extern "C" {
 
 // Sizes shared by the routing, layout, dispatch and combine entry points: a
@@ -878,12 +901,10 @@ int fp8_moe_route_bwd(const void* logits, int logits_bf16, int64_t T, int64_t E,
   if (rc) return rc;
   RouteBwdArgs a{logits, ids, dweights, dlogits, T, static_cast<int32_t>(E), static_cast<int32_t>(top_k),
                  sigmoid != 0, renorm != 0, scale};
-  const unsigned grid = static_cast<unsigned>((T + kRouteWarps - 1) / kRouteWarps);
-  const size_t smem = static_cast<size_t>(kRouteWarps) * E * sizeof(float);
   if (logits_bf16)
-    moe_route_bwd_kernel<true><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
+    launch_route_bwd<true>(a, dev->num_sms, stream);
   else
-    moe_route_bwd_kernel<false><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
+    launch_route_bwd<false>(a, dev->num_sms, stream);
   return launched();
 }
 
@@ -891,9 +912,24 @@ static int run_layout(const LayoutArgs& a, cudaStream_t stream) {
   DeviceInfo* dev = nullptr;
   int rc = device_info(&dev);
   if (rc) return rc;
-  const int64_t ctas = (a.n + kLayoutThreads - 1) / kLayoutThreads;
-  moe_layout_kernel<<<static_cast<unsigned>(ctas ? ctas : 1), kLayoutThreads, 0, stream>>>(a);
-  return launched();
+  // one cluster: a CTA per 1024 entries, up to eight
+  unsigned ctas = 1;
+  while (ctas < kLayoutMaxCtas && static_cast<int64_t>(ctas) * kLayoutThreads < a.n) ctas *= 2;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = ctas;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kLayoutThreads);
+  cfg.dynamicSmemBytes = layout_smem(a.E);
+  cfg.stream = stream;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, moe_layout_kernel, a) != cudaSuccess) return FP8Q_ERR_CUDA;
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return FP8Q_OK;
 }
 
 int fp8_moe_layout_contiguous(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* slots,

@@ -11,151 +11,31 @@
 // operand from saved 1x128 tiles.
 #pragma once
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cstdint>
 
+#include "fp8q_codes.cuh"
 #include "fp8q_ptx.cuh"
 #include "fp8q_quant.cuh"
 
 namespace fp8q {
 
-// ------------------------------------------------------------ packed FP32
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t join_f32x2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void split_f32x2(uint64_t p, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
-}
-__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// Four E4M3 codes -> their values (exact), two packed pairs.
-__device__ __forceinline__ void e4m3x4_to_f32x2(uint32_t c, uint64_t& p0, uint64_t& p1) {
-  uint32_t h0, h1;
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "mov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(h0), "=r"(h1)
-      : "r"(c));
-  const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-  const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-  p0 = join_f32x2(f0.x, f0.y);
-  p1 = join_f32x2(f1.x, f1.y);
-}
-
-// ------------------------------------------------------------ codes by a corrected quotient
-// The code of fl32(x / s) without a division, a bracket or a branch: with
-// y = RN(1/s), q0 = x y, q1 = q0 + (x - q0 s) y.  Away from the E4M3 midpoints
-// q1 and fl32(x / s) are on the same side of each.  They could part only where
-// x / s is next to an FP32 rounding midpoint beside an E4M3 midpoint; there q0
-// is one of the two floats around it (x y is off by less than an ulp), x - q0 s
-// is exact, and what is left of y's error is below 2^-25 ulp, while x / s, a
-// quotient of two 24-bit numbers, is at least 2^-24 ulp away.  The same holds
-// for bf16 and for FP32 values x.  Needs y within half an ulp of 1/s, checked
-// exactly (1 - s y is a float), and s far from the ends of the range, so that no
-// remainder underflows where a code is decided; else the IEEE division.
-//
-// y is kept negated: with -q0 and -q1 a zero keeps its sign, and one XOR turns
-// four codes' signs back.  Three packed FP32 operations and one conversion a
-// pair of elements, against two products, two conversions and a comparison for
-// the bracket, and no element is ever redone.
-struct DivScale {
-  uint64_t ny2, s2;  // {-y, -y} and {s, s}
-  bool ok;
-};
-__device__ __forceinline__ bool corrected_reciprocal(float s, float& y) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  y = __fmaf_rn(r, __fmaf_rn(-s, r, 1.0f), r);
-  const float half_ulp = __uint_as_float(__float_as_uint(y) & 0x7F800000u) * 0x1p-24f;
-  return fabsf(__fmaf_rn(-s, y, 1.0f)) <= s * half_ulp && s >= 0x1p-80f && s <= 0x1p+120f;
-}
-__device__ __forceinline__ DivScale div_scale(float s) {
-  float y;
-  const bool ok = corrected_reciprocal(s, y);
-  return {pack_f32x2(-y), pack_f32x2(s), ok};
-}
-// -(x / s), corrected, for a pair.
-__device__ __forceinline__ uint64_t neg_quotient(uint64_t x, uint64_t ny2, uint64_t s2) {
-  const uint64_t q0 = mul_f32x2(x, ny2);
-  return fma_f32x2(fma_f32x2(q0, s2, x), ny2, q0);
-}
-__device__ __forceinline__ uint32_t codes4(uint64_t x0, uint64_t x1, const DivScale& d) {
-  return e4m3x4_from_f32x2(neg_quotient(x0, d.ny2, d.s2), neg_quotient(x1, d.ny2, d.s2)) ^ 0x80808080u;
-}
-// Codes of fl32(x / s) for four FP32 values by IEEE division.
-__device__ __noinline__ uint32_t codes4_exact(uint64_t x0, uint64_t x1, float s) {
-  float a, b, c, d;
-  split_f32x2(x0, a, b);
-  split_f32x2(x1, c, d);
-  return cvt_e4m3x2(__fdiv_rn(a, s), __fdiv_rn(b, s)) | (cvt_e4m3x2(__fdiv_rn(c, s), __fdiv_rn(d, s)) << 16);
-}
-// 16 bf16 (eight words) -> 16 codes, low byte first.
-__device__ __forceinline__ uint4 codes16_bf16(const uint32_t (&w)[8], float s) {
-  const DivScale d = div_scale(s);
-  if (!d.ok) return quantize16_exact(w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7], s);
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = codes4(bf16x2_to_f32x2(w[2 * i]), bf16x2_to_f32x2(w[2 * i + 1]), d);
-  return make_uint4(c[0], c[1], c[2], c[3]);
-}
-// 16 FP32 values (eight pairs) -> 16 codes.
-__device__ __forceinline__ uint4 codes16_f32(const uint64_t (&v)[8], float s) {
-  const DivScale d = div_scale(s);
-  uint32_t c[4];
-  if (d.ok) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = codes4(v[2 * i], v[2 * i + 1], d);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = codes4_exact(v[2 * i], v[2 * i + 1], s);
-  }
-  return make_uint4(c[0], c[1], c[2], c[3]);
-}
-
-// s = fl32(amax / 448), 1 when that is 0, for any finite FP32 amax.
-__device__ __forceinline__ float group_scale_f32(float amax) {
-  const float s = __fdiv_rn(amax, 448.0f);
-  return s == 0.0f ? 1.0f : s;
-}
-
 // ------------------------------------------------------------ exp(-g) for a pair
 // e^x = 2^(x L) with L = log2 e: t = fl(x L), and what t lacks, x L - t =
 // fma(x, L, -t) + x (log2 e - L), enters as a factor 1 + ln 2 times it.  With
-// ex2.approx (2^-22) the result is within 2^-21.9.  x = -g is held to
-// [-100, 88]: below, e^x counts for nothing beside 1; above, 1 / (1 + e^x) is 0
-// (flushed), which the callers treat as out of range.
-__device__ __forceinline__ uint64_t exp_neg_f32x2(uint64_t g2) {
-  float g0, g1;
-  split_f32x2(g2, g0, g1);
-  const uint64_t x = join_f32x2(fminf(fmaxf(-g0, -100.0f), 88.0f), fminf(fmaxf(-g1, -100.0f), 88.0f));
+// ex2.approx (2^-22) the result is within 2^-21.9.  For g in [-88, 2^126]: at the
+// lower end 1 / (1 + e) is 0 (flushed), at the upper e is.
+__device__ __forceinline__ uint64_t exp_neg_f32x2(uint64_t g) {
   constexpr float kL = 1.44269504f;  // nearest FP32 to log2 e, 1.925963e-8 below it
-  const uint64_t nt = mul_f32x2(x, pack_f32x2(-kL));
-  uint64_t r = fma_f32x2(x, pack_f32x2(kL), nt);
-  r = fma_f32x2(x, pack_f32x2(1.925963e-8f), r);
+  const uint64_t t = mul_f32x2(g, pack_f32x2(-kL));
+  // what t lacks, negated: g L + t + g (log2 e - L)
+  uint64_t r = fma_f32x2(g, pack_f32x2(kL), t);
+  r = fma_f32x2(g, pack_f32x2(1.925963e-8f), r);
   float t0, t1, e0, e1;
-  split_f32x2(nt, t0, t1);
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(-t0));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(-t1));
+  split_f32x2(t, t0, t1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
   const uint64_t e = join_f32x2(e0, e1);
-  return fma_f32x2(e, mul_f32x2(r, pack_f32x2(0.693147181f)), e);
+  return fma_f32x2(e, mul_f32x2(r, pack_f32x2(-0.693147181f)), e);
 }
 // 1 / (1 + e) by rcp.approx.ftz (1 ulp).
 __device__ __forceinline__ uint64_t rcp_one_plus(uint64_t e) {
@@ -170,25 +50,28 @@ __device__ __forceinline__ uint64_t rcp_one_plus(uint64_t e) {
 // same values as swiglu16.  FP32: exp 2^-21.9 (weighted by 1 - p), 1 + e 2^-24,
 // rcp 2^-23, two products 2^-23: below 2^-20.8.  Where h (1 -+ 1.375 * 2^-21),
 // their roundings counted, give one bf16, that is it; elements they leave open
-// (about one in 3000), and those outside [2^-100, 2^120], are evaluated in
-// double, their words read again at gp and up.
-__device__ __forceinline__ void swiglu16_f32x2(const uint32_t (&gw)[8], const uint32_t (&uw)[8], uint32_t (&hw)[8],
-                                               const uint8_t* gp, const uint8_t* up) {
+// (about one in 3000), and those outside [2^-99, 2^119], are evaluated in
+// double, their words read again at gp and up.  Gates below -88 enter as -88,
+// where h comes out as 0 and is evaluated in double; lanes with a gate above
+// 2^126 (g_max, the lane's largest magnitude) are too.  Returns the largest |h|.
+__device__ __forceinline__ float swiglu16_f32x2(const uint32_t (&gw)[8], const uint32_t (&uw)[8], uint32_t (&hw)[8],
+                                                float g_max, const uint8_t* gp, const uint8_t* up) {
   uint32_t d[8];
   uint32_t any = 0u, most = 0u, least = 0x7F807F80u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint64_t g = bf16x2_to_f32x2(gw[i]), u = bf16x2_to_f32x2(uw[i]);
+    const uint64_t g = bf16x2_to_f32x2(max_bf16x2(gw[i], 0xC2B0C2B0u)), u = bf16x2_to_f32x2(uw[i]);  // -88
     const uint64_t h = mul_f32x2(mul_f32x2(g, rcp_one_plus(exp_neg_f32x2(g))), u);
     hw[i] = bf16x2_from_pair(mul_f32x2(h, pack_f32x2(1.0f - 0x1.6p-21f)));
     d[i] = hw[i] ^ bf16x2_from_pair(mul_f32x2(h, pack_f32x2(1.0f + 0x1.6p-21f)));
     any |= d[i];
-    most = max_bf16x2(most, hw[i] & 0x7FFF7FFFu);
-    least = min_bf16x2(least, hw[i] & 0x7FFF7FFFu);
+    const uint32_t m = hw[i] & 0x7FFF7FFFu;
+    most = max_bf16x2(most, m);
+    least = min_bf16x2(least, m);
   }
-  // bf16 bounds well inside the range where the error bound holds (NaN fails)
-  const bool in_range = max(most & 0xFFFFu, most >> 16) <= 0x7B00u && min(least & 0xFFFFu, least >> 16) >= 0x0E00u;
-  if (any == 0u && in_range) return;
+  const uint32_t top = max(most & 0xFFFFu, most >> 16);
+  const bool in_range = top <= 0x7B00u && min(least & 0xFFFFu, least >> 16) >= 0x0E00u && g_max < 0x1p+126f;
+  if (any == 0u && in_range) return __uint_as_float(top << 16);
   uint32_t redo = 0u;  // bit 2i + j: half j of word i
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -201,6 +84,7 @@ __device__ __forceinline__ void swiglu16_f32x2(const uint32_t (&gw)[8], const ui
       redo |= static_cast<uint32_t>(open) << (2 * i + j);
     }
   }
+  if (!(g_max < 0x1p+126f)) redo = 0xFFFFu;
   for (; redo != 0u; redo &= redo - 1u) {
     const int b = __ffs(redo) - 1, i = b >> 1, sh = (b & 1) * 16;
     const uint32_t g = __ldg(reinterpret_cast<const uint32_t*>(gp) + i) >> sh << 16;
@@ -209,6 +93,7 @@ __device__ __forceinline__ void swiglu16_f32x2(const uint32_t (&gw)[8], const ui
 #pragma unroll
     for (int k = 0; k < 8; ++k) hw[k] = i == k ? (hw[k] & (0xFFFF0000u >> sh)) | x : hw[k];
   }
+  return abs_max16(hw);
 }
 
 // ---------------------------------------------------------------------------
@@ -234,16 +119,14 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_1x128_kernel(const uint8_t
     const uint32_t kb = valid ? static_cast<uint32_t>(t) - row * per_row : 0u;
     const int64_t gate = static_cast<int64_t>(row) * 2 * inter + static_cast<int64_t>(kb) * 128 + sub * 16;
     uint32_t gw[8], uw[8], hw[8];
+    float ah = 0.0f, ag = 0.0f, au = 0.0f;
     if (valid) {
       ld_nc_v8(c1 + gate * 2, gw);
       ld_nc_v8(c1 + (gate + inter) * 2, uw);
-      swiglu16_f32x2(gw, uw, hw, c1 + gate * 2, c1 + (gate + inter) * 2);
-    } else {
-      zero8(gw);
-      zero8(uw);
-      zero8(hw);
+      ag = abs_max16(gw);
+      au = abs_max16(uw);
+      ah = swiglu16_f32x2(gw, uw, hw, ag, c1 + gate * 2, c1 + (gate + inter) * 2);
     }
-    float ah = abs_max16(hw), ag = abs_max16(gw), au = abs_max16(uw);
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) {
       ah = fmaxf(ah, __shfl_xor_sync(0xFFFFFFFFu, ah, off));
@@ -407,13 +290,16 @@ __global__ void __launch_bounds__(128, 5) ckpt_128x1_t_kernel(const uint8_t* __r
   const int64_t tok0 = mb * 128 + rg * 8;
   uint2 c[8];
   float sr[8];
+  const uint8_t* qp = q + tok0 * K + kc * kCkptChannels + cg * 8;
+  const float* sp = s + tok0 * (K >> 7) + (kc >> 1);
+  const int left = M - tok0 < 8 ? static_cast<int>(M - tok0) : 8;
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
+  for (int r = 0; r < 8; ++r, qp += K, sp += K >> 7) {
     c[r] = make_uint2(0u, 0u);
     sr[r] = 1.0f;
-    if (tok0 + r < M) {
-      c[r] = __ldg(reinterpret_cast<const uint2*>(q + (tok0 + r) * K + kc * kCkptChannels + cg * 8));
-      sr[r] = __ldg(s + (tok0 + r) * (K >> 7) + (kc >> 1));
+    if (r < left) {
+      c[r] = __ldg(reinterpret_cast<const uint2*>(qp));
+      sr[r] = __ldg(sp);
     }
   }
   uint64_t v[8][4];  // [token][channel pair]

@@ -9,11 +9,13 @@
 // (a)); these kernels produce and consume those layouts.
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
 
+#include "fp8q_codes.cuh"
 #include "fp8q_ptx.cuh"
 #include "fp8q_quant.cuh"
 
@@ -520,7 +522,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_f64_kernel(RouteAr
 // nothing; an id that appears twice gets the sum.  1 - p_j is evaluated as
 // 1 / (1 + exp(l_j)), which keeps its digits when p_j is close to 1.
 //
-// One warp per token; the row of gradients is gathered in shared memory.
+// One warp per token.  The chosen experts' values are scattered into a row of
+// shared memory and read back in expert order; only the dense form reads the
+// whole row of logits, once, into registers.  Warps walk the rows at a stride of
+// the grid.
 // ---------------------------------------------------------------------------
 struct RouteBwdArgs {
   const void* logits;
@@ -532,76 +537,93 @@ struct RouteBwdArgs {
   float scale;
 };
 
-template <bool kBf16>
+// VPL: experts of a lane (lane, lane + 32, ...), E <= 32 VPL; kDense: softmax
+// without renorm, where every logit gets a gradient.
+template <int VPL, bool kBf16, bool kDense>
 __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_bwd_kernel(RouteBwdArgs a) {
   extern __shared__ float route_grad[];  // [kRouteWarps][E]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-  if (t >= a.T) return;
   const int E = a.E;
-  const void* row = logits_row<kBf16>(a.logits, t, E);
   float* d = route_grad + static_cast<int64_t>(warp) * E;
-  for (int e = lane; e < E; e += 32) d[e] = 0.0f;
-  int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
-  if (id >= E) id = -1;
-  float g = 0.0f, l = neg_inf_f32();
-  if (id >= 0) {
-    g = a.dweights[t * a.top_k + lane];
-    l = load_logit<kBf16>(row, id);
-  }
-  const bool has = id >= 0 && l > neg_inf_f32();
-  const bool dense = !a.sigmoid && !a.renorm;
-  float v = g;  // dense: the gradient of p; else of the logit
-  if (!dense) {
-    const float not_p = a.sigmoid ? 1.0f / (1.0f + expf(l)) : 1.0f;
-    if (a.renorm) {
-      const float r = route_weight(l, has, a.sigmoid, true, 1.0f, 0.0f, 1.0f);
-      const float mean = warp_sum(has ? g * r : 0.0f);
-      v = a.scale * r * (g - mean) * not_p;
-    } else {
-      v = a.scale * g * (1.0f / (1.0f + expf(-l))) * not_p;
-    }
-  }
-  if (!has) v = 0.0f;
-  // an id that appears more than once: the sum, in place order
-  const uint32_t same = __match_any_sync(0xFFFFFFFFu, has ? id : -1 - lane);
-  if (__any_sync(0xFFFFFFFFu, __popc(same) > 1)) {
-    float total = 0.0f;
-    for (int j = 0; j < a.top_k; ++j) {
-      const float o = __shfl_sync(0xFFFFFFFFu, v, j);
-      if ((same >> j) & 1u) total += o;
-    }
-    v = total;
-  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (i * 32 + lane < E) d[i * 32 + lane] = 0.0f;
   __syncwarp();
-  if (has) d[id] = v;
-  __syncwarp();
-  float row_max = neg_inf_f32(), inv_sum = 0.0f, mean = 0.0f;
-  if (dense) {
-    float sum = 0.0f, dot = 0.0f;
-    for (int e = lane; e < E; e += 32) row_max = fmaxf(row_max, load_logit<kBf16>(row, e));
-    row_max = warp_max(row_max);
-    for (int e = lane; e < E; e += 32) {
-      const float x = load_logit<kBf16>(row, e);
-      const float p = x > neg_inf_f32() ? expf(x - row_max) : 0.0f;
-      sum += p;
-      dot += p * d[e];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp; t < a.T; t += step) {
+    const void* row = logits_row<kBf16>(a.logits, t, E);
+    float x[kDense ? VPL : 1];
+    if constexpr (kDense) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) x[i] = i * 32 + lane < E ? load_logit<kBf16>(row, i * 32 + lane) : neg_inf_f32();
     }
-    sum = warp_sum(sum);
-    dot = warp_sum(dot);
-    inv_sum = sum > 0.0f ? 1.0f / sum : 0.0f;
-    mean = dot * inv_sum;
-  }
-  for (int e = lane; e < E; e += 32) {
-    float o = d[e];
-    if (dense) {
-      const float x = load_logit<kBf16>(row, e);
-      o = x > neg_inf_f32() ? a.scale * (expf(x - row_max) * inv_sum) * (o - mean) : 0.0f;
+    int id = lane < a.top_k ? __ldg(a.ids + t * a.top_k + lane) : -1;
+    if (id >= E) id = -1;
+    float g = 0.0f, l = neg_inf_f32();
+    if (id >= 0) {
+      g = __ldg(a.dweights + t * a.top_k + lane);
+      l = load_logit<kBf16>(row, id);
     }
-    if constexpr (kBf16)
-      static_cast<__nv_bfloat16*>(a.dlogits)[t * E + e] = __float2bfloat16_rn(o);
-    else
-      static_cast<float*>(a.dlogits)[t * E + e] = o;
+    const bool has = id >= 0 && l > neg_inf_f32();
+    float v = g;  // dense: the gradient of p; else of the logit
+    if constexpr (!kDense) {
+      const float not_p = a.sigmoid ? 1.0f / (1.0f + expf(l)) : 1.0f;
+      if (a.renorm) {
+        const float r = route_weight(l, has, a.sigmoid, true, 1.0f, 0.0f, 1.0f);
+        const float mean = warp_sum(has ? g * r : 0.0f);
+        v = a.scale * r * (g - mean) * not_p;
+      } else {
+        v = a.scale * g * (1.0f / (1.0f + expf(-l))) * not_p;
+      }
+    }
+    if (!has) v = 0.0f;
+    // an id that appears more than once: the sum, in place order
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, has ? id : -1 - lane);
+    if (__any_sync(0xFFFFFFFFu, __popc(same) > 1)) {
+      float total = 0.0f;
+      for (int j = 0; j < a.top_k; ++j) {
+        const float o = __shfl_sync(0xFFFFFFFFu, v, j);
+        if ((same >> j) & 1u) total += o;
+      }
+      v = total;
+    }
+    if (has) d[id] = v;
+    __syncwarp();
+    float o[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) o[i] = i * 32 + lane < E ? d[i * 32 + lane] : 0.0f;
+    __syncwarp();
+    if (has) d[id] = 0.0f;  // for the next row
+    __syncwarp();
+    if constexpr (kDense) {
+      float m = neg_inf_f32();
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
+      m = value_of(redux_max(key_of(m)));  // of logits without NaN
+      float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        x[i] = x[i] > neg_inf_f32() ? expf(x[i] - m) : 0.0f;
+        sum += x[i];
+        dot = fmaf(x[i], o[i], dot);
+      }
+      sum = warp_sum(sum);
+      dot = warp_sum(dot);
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float mean = dot * inv;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) o[i] = a.scale * (x[i] * inv) * (o[i] - mean);
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * 32 + lane;
+      if (e < E) {
+        if constexpr (kBf16)
+          static_cast<__nv_bfloat16*>(a.dlogits)[t * E + e] = __float2bfloat16_rn(o[i]);
+        else
+          static_cast<float*>(a.dlogits)[t * E + e] = o[i];
+      }
+    }
   }
 }
 
@@ -613,11 +635,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_bwd_kernel(RouteBw
 // rank being the number of earlier entries with the same expert, so the layout
 // does not depend on any order of execution.  Ids outside [0, E) get no row.
 //
-// One CTA per 1024 entries.  Each counts the experts of all entries, those
-// before its own apart (integer shared-memory atomics: their order does not
-// change a count), then ranks its own: __match_any within a warp, a byte
-// table [warp][expert] across warps.  One launch and no workspace, at the
-// price of every CTA reading all ids.
+// One cluster of up to eight CTAs (1024 threads each) takes all entries; every
+// warp owns one run of consecutive entries.  It counts its run's experts into
+// its own row of a shared table (__match_any groups equal ids of 32 entries, so
+// no two lanes touch one counter), the table's columns are turned into exclusive
+// prefixes over the warps, the CTAs' totals are read from one another's shared
+// memory, and the warps walk their runs once more, handing out ranks.  One
+// launch, no workspace, no atomics, and the entries are read twice.
 // ---------------------------------------------------------------------------
 struct LayoutArgs {
   const int32_t* ids;
@@ -631,34 +655,67 @@ struct LayoutArgs {
 };
 
 constexpr int kLayoutThreads = 1024;
+constexpr int kLayoutWarps = kLayoutThreads / 32;
+constexpr int kLayoutMaxCtas = 8;  // the portable cluster size
+constexpr int kLayoutAhead = 4;    // groups of 32 entries loaded together
+constexpr int layout_smem(int E) { return kLayoutWarps * E * 4; }
 
 __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(LayoutArgs a) {
-  __shared__ int32_t before[kMaxExperts];  // entries of each expert ahead of this CTA's
-  __shared__ int32_t all[kMaxExperts];     // the others; then all entries
-  __shared__ int32_t start[kMaxExperts + 1];
-  __shared__ uint8_t in_warp[32][kMaxExperts];
-  __shared__ int32_t warp_total[32];
+  extern __shared__ int32_t layout_table[];  // [kLayoutWarps][E]
+  __shared__ int32_t hist[kMaxExperts];      // this CTA's entries of each expert
+  __shared__ int32_t before[kMaxExperts];    // entries in the CTAs ahead
+  __shared__ int32_t start[kMaxExperts + 1]; // contiguous: first block of each expert
+  __shared__ int32_t warp_total[kLayoutWarps];
+  const auto cluster = cooperative_groups::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int E = a.E;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kLayoutThreads;
-  before[tid] = 0;
-  all[tid] = 0;
-  for (int e = tid; e < 32 * kMaxExperts / 4; e += kLayoutThreads) reinterpret_cast<uint32_t*>(in_warp)[e] = 0u;
+  int32_t* mine = layout_table + warp * E;
+  // groups of 32 entries of a warp, and its first entry
+  const int64_t per_cta = kLayoutWarps * 32 * static_cast<int64_t>(gridDim.x);
+  const int64_t groups = (a.n + per_cta - 1) / per_cta;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kLayoutWarps + warp) * groups * 32 + lane;
+  auto expert = [&](int64_t g) {
+    const int64_t i = first + g * 32;
+    const int e = g < groups && i < a.n ? __ldg(a.ids + i) : -1;
+    return static_cast<uint32_t>(e) < static_cast<uint32_t>(E) ? e : -1;
+  };
+  for (int i = tid; i < kLayoutWarps * E; i += kLayoutThreads) layout_table[i] = 0;
   __syncthreads();
-  for (int64_t i = tid; i < a.n; i += kLayoutThreads) {
-    const int e = a.ids[i];
-    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E)) atomicAdd(i < first ? &before[e] : &all[e], 1);
+  for (int64_t g = 0; g < groups; g += kLayoutAhead) {
+    int e[kLayoutAhead];
+#pragma unroll
+    for (int k = 0; k < kLayoutAhead; ++k) e[k] = expert(g + k);
+#pragma unroll
+    for (int k = 0; k < kLayoutAhead; ++k) {
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e[k]);
+      if (e[k] >= 0 && lane == __ffs(same) - 1) mine[e[k]] += __popc(same);
+      __syncwarp();
+    }
   }
-  const int64_t mine = first + tid;
-  int e = mine < a.n ? a.ids[mine] : -1;
-  if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(E)) e = -1;
-  const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-  int rank = __popc(same & ((1u << lane) - 1u));
-  if (e >= 0 && rank == 0) in_warp[warp][e] = static_cast<uint8_t>(__popc(same));
   __syncthreads();
-  // whole entries of expert tid, and the exclusive prefix of the experts' rows
-  const int count = tid < E ? before[tid] + all[tid] : 0;
-  const int size = (count + 127) >> 7;  // blocks of 128 rows
+  if (tid < E) {
+    int32_t sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < kLayoutWarps; ++w) {
+      const int32_t c = layout_table[w * E + tid];
+      layout_table[w * E + tid] = sum;
+      sum += c;
+    }
+    hist[tid] = sum;
+  }
+  cluster.sync();
+  int32_t ahead = 0, count = 0;
+  if (tid < E) {
+    for (unsigned r = 0; r < gridDim.x; ++r) {
+      const int32_t h = *cluster.map_shared_rank(&hist[tid], r);
+      if (r < blockIdx.x) ahead += h;
+      count += h;
+    }
+    before[tid] = ahead;
+  }
+  cluster.sync();  // no CTA may end while another reads its counts
+  // exclusive prefix of the experts' blocks of 128 rows
+  const int size = (count + 127) >> 7;
   int incl = size;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -680,23 +737,32 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(LayoutArgs a
   __syncthreads();
   start[tid] = warp_total[warp] + incl - size;
   if (tid == kLayoutThreads - 1) start[kMaxExperts] = warp_total[warp] + incl;
-  __syncthreads();
-  if (mine < a.n) {
-    int64_t slot = -1;
-    if (e >= 0) {
-      for (int w = 0; w < warp; ++w) rank += in_warp[w][e];
-      const int64_t r = static_cast<int64_t>(before[e]) + rank;
-      if (a.cap > 0)
-        slot = r < a.cap ? e * a.cap + r : -1;
-      else
-        slot = static_cast<int64_t>(start[e]) * 128 + r;
-    }
-    a.slots[mine] = static_cast<int32_t>(slot);
-  }
   if (blockIdx.x == 0 && tid < E)
     a.counts[tid] = a.cap > 0 && count > a.cap ? static_cast<int32_t>(a.cap) : count;
+  __syncthreads();
+  for (int64_t g = 0; g < groups; g += kLayoutAhead) {
+    int e[kLayoutAhead];
+#pragma unroll
+    for (int k = 0; k < kLayoutAhead; ++k) e[k] = expert(g + k);
+#pragma unroll
+    for (int k = 0; k < kLayoutAhead; ++k) {
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e[k]);
+      int64_t slot = -1;
+      if (e[k] >= 0) {
+        const int64_t r = static_cast<int64_t>(before[e[k]]) + mine[e[k]] + __popc(same & ((1u << lane) - 1u));
+        if (a.cap > 0)
+          slot = r < a.cap ? e[k] * a.cap + r : -1;
+        else
+          slot = static_cast<int64_t>(start[e[k]]) * 128 + r;
+      }
+      __syncwarp();
+      if (e[k] >= 0 && lane == __ffs(same) - 1) mine[e[k]] += __popc(same);
+      __syncwarp();
+      if (g + k < groups && first + (g + k) * 32 < a.n) a.slots[first + (g + k) * 32] = static_cast<int32_t>(slot);
+    }
+  }
   if (a.cap == 0) {
-    // the expert of each block: the last whose first block is not past it and that has blocks
+    // the expert of each block: the last whose first block is not past it
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kLayoutThreads;
     for (int64_t b = static_cast<int64_t>(blockIdx.x) * kLayoutThreads + tid; b < a.blocks; b += stride) {
       int owner = -1;
@@ -767,9 +833,8 @@ __global__ void __launch_bounds__(256, 5) moe_dispatch_1x128_kernel(DispatchArgs
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
     const float sc = group_scale(amax);
-    const RecipPair rp = recip_pair(sc);
     if (valid) {
-      const uint4 codes = quantize16(v, sc, rp, sc < kMinFastScale);
+      const uint4 codes = codes16_bf16(v, sc);
       const uint32_t tok = static_cast<uint32_t>(t) / static_cast<uint32_t>(a.nkb);
       const uint32_t kb = static_cast<uint32_t>(t) - tok * static_cast<uint32_t>(a.nkb);
       const int32_t* sl = a.slots + static_cast<int64_t>(tok) * a.top_k;
@@ -823,6 +888,8 @@ __device__ __forceinline__ void fma8_bf16(float (&acc)[8], const uint4& v, float
   }
 }
 
+constexpr int kCombineEntries = 4;  // rows of a token loaded together
+
 __global__ void __launch_bounds__(256) moe_combine_kernel(CombineArgs a) {
   const int sub = threadIdx.x & 15;  // eight channels of a 128-channel tile
   const int64_t stride = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 4;
@@ -833,10 +900,23 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(CombineArgs a) {
     const int64_t e0 = static_cast<int64_t>(tok) * a.top_k;
     const int64_t col = static_cast<int64_t>(kb) * 128 + sub * 8;
     float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < a.top_k; ++j) {
-      const int64_t row = __ldg(a.slots + e0 + j);
-      if (row >= 0 && row < a.rows)
-        fma8_bf16(acc, ld_nc_v4(a.y + (row * D + col) * 2), a.weights != nullptr ? __ldg(a.weights + e0 + j) : 1.0f);
+    for (int j0 = 0; j0 < a.top_k; j0 += kCombineEntries) {
+      uint4 v[kCombineEntries];
+      float w[kCombineEntries];
+#pragma unroll
+      for (int j = 0; j < kCombineEntries; ++j) {
+        v[j] = make_uint4(0u, 0u, 0u, 0u);
+        w[j] = 0.0f;
+        if (j0 + j < a.top_k) {
+          const int64_t row = __ldg(a.slots + e0 + j0 + j);
+          if (row >= 0 && row < a.rows) {
+            v[j] = ld_nc_v4(a.y + (row * D + col) * 2);
+            w[j] = a.weights != nullptr ? __ldg(a.weights + e0 + j0 + j) : 1.0f;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kCombineEntries; ++j) fma8_bf16(acc, v[j], w[j]);
     }
     *reinterpret_cast<uint4*>(a.out + t * 256 + sub * 16) =
         make_uint4(bf16x2_rn(acc[0], acc[1]), bf16x2_rn(acc[2], acc[3]), bf16x2_rn(acc[4], acc[5]),
@@ -890,7 +970,7 @@ __device__ __forceinline__ uint4 scale8_bf16(const uint4& v, float w) {
 constexpr int kCombineBwdThreads = 256;
 constexpr int kCombineBwdEntries = 8;  // entries of a token handled at once
 
-__global__ void __launch_bounds__(kCombineBwdThreads) moe_combine_bwd_kernel(CombineBwdArgs a) {
+__global__ void __launch_bounds__(kCombineBwdThreads, 3) moe_combine_bwd_kernel(CombineBwdArgs a) {
   constexpr int kWarps = kCombineBwdThreads / 32;
   __shared__ float part[kWarps][kCombineBwdEntries];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -898,27 +978,31 @@ __global__ void __launch_bounds__(kCombineBwdThreads) moe_combine_bwd_kernel(Com
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     const uint8_t* dout = a.dout + t * a.D * 2;
     for (int j0 = 0; j0 < a.top_k; j0 += kCombineBwdEntries) {
-      int64_t row[kCombineBwdEntries];
+      int32_t row[kCombineBwdEntries];
       float w[kCombineBwdEntries], acc[kCombineBwdEntries];
 #pragma unroll
       for (int j = 0; j < kCombineBwdEntries; ++j) {
         row[j] = -1;
         w[j] = acc[j] = 0.0f;
         if (j0 + j < a.top_k) {
-          const int64_t r = __ldg(a.slots + t * a.top_k + j0 + j);
+          const int32_t r = __ldg(a.slots + t * a.top_k + j0 + j);
           if (r >= 0 && r < a.rows) row[j] = r;
           w[j] = __ldg(a.weights + t * a.top_k + j0 + j);
         }
       }
       for (int64_t c = tid; c < chunks; c += kCombineBwdThreads) {
         const uint4 g = ld_nc_v4(dout + c * 16);
+        uint4 v[kCombineBwdEntries];  // all rows' loads before any is used
 #pragma unroll
         for (int j = 0; j < kCombineBwdEntries; ++j) {
-          if (row[j] >= 0) {
-            const int64_t at = (row[j] * a.D + c * 8) * 2;
-            acc[j] = dot8_bf16(acc[j], g, ld_nc_v4(a.y + at));
-            *reinterpret_cast<uint4*>(a.dy + at) = scale8_bf16(g, w[j]);
-          }
+          v[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (row[j] >= 0) v[j] = ld_nc_v4(a.y + (row[j] * a.D + c * 8) * 2);
+        }
+#pragma unroll
+        for (int j = 0; j < kCombineBwdEntries; ++j) {
+          if (row[j] < 0) continue;
+          acc[j] = dot8_bf16(acc[j], g, v[j]);
+          *reinterpret_cast<uint4*>(a.dy + (row[j] * a.D + c * 8) * 2) = scale8_bf16(g, w[j]);
         }
       }
 #pragma unroll
