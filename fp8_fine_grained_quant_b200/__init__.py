@@ -84,8 +84,9 @@ EXPORTS = {
     "fp8_gemm_wgrad": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
     "fp8_moe_route": (ctypes.c_int, [_P, _INT, _I64, _I64, _P, _INT, _I64, _I64, _I64, _I64, _INT, _FLT, _P, _P, _P]),
     "fp8_moe_route_bwd": (ctypes.c_int, [_P, _INT, _I64, _I64, _P, _P, _INT, _I64, _INT, _FLT, _P, _P]),
-    "fp8_moe_layout_contiguous": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P, _P]),
-    "fp8_moe_layout_masked": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _P, _P, _P]),
+    "fp8_moe_layout_contiguous": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
+    "fp8_moe_layout_masked": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "fp8_moe_layout_workspace": (_I64, [_I64, _I64, _I64]),
     "fp8_moe_dispatch_1x128": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P]),
     "fp8_moe_combine": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _I64, _I64, _P, _P]),
     "fp8_moe_combine_bwd": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P]),

@@ -817,24 +817,24 @@ static void launch_route(const RouteArgs& a, int num_sms, cudaStream_t stream) {
   }
 }
 
+// The instance with the fewest experts a lane: exact up to 256 experts (a row of
+// 160 in the 8-a-lane instance costs a third more than in its own), in steps
+// above.
 template <int VPL, bool kBf16>
-static void launch_route_bwd_vpl(const RouteBwdArgs& a, int num_sms, cudaStream_t stream) {
-  const int64_t ctas = (a.T + kRouteWarps - 1) / kRouteWarps, cap = static_cast<int64_t>(num_sms) * 16;
-  const unsigned grid = static_cast<unsigned>(ctas < cap ? ctas : cap);
+static void launch_route_bwd(const RouteBwdArgs& a, cudaStream_t stream) {
+  if constexpr (VPL < 32) {
+    if (a.E > 32 * VPL) {
+      constexpr int kNext = VPL < 8 ? VPL + 1 : (VPL < 16 ? 16 : 32);
+      launch_route_bwd<kNext, kBf16>(a, stream);
+      return;
+    }
+  }
+  const unsigned grid = static_cast<unsigned>((a.T + kRouteWarps - 1) / kRouteWarps);
   const size_t smem = static_cast<size_t>(kRouteWarps) * a.E * sizeof(float);
   if (!a.sigmoid && !a.renorm)
     moe_route_bwd_kernel<VPL, kBf16, true><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
   else
     moe_route_bwd_kernel<VPL, kBf16, false><<<grid, 32 * kRouteWarps, smem, stream>>>(a);
-}
-template <bool kBf16>
-static void launch_route_bwd(const RouteBwdArgs& a, int num_sms, cudaStream_t stream) {
-  if (a.E <= 64)
-    launch_route_bwd_vpl<2, kBf16>(a, num_sms, stream);
-  else if (a.E <= 256)
-    launch_route_bwd_vpl<8, kBf16>(a, num_sms, stream);
-  else
-    launch_route_bwd_vpl<32, kBf16>(a, num_sms, stream);
 }
 
 extern "C" {
@@ -902,16 +902,33 @@ int fp8_moe_route_bwd(const void* logits, int logits_bf16, int64_t T, int64_t E,
   RouteBwdArgs a{logits, ids, dweights, dlogits, T, static_cast<int32_t>(E), static_cast<int32_t>(top_k),
                  sigmoid != 0, renorm != 0, scale};
   if (logits_bf16)
-    launch_route_bwd<true>(a, dev->num_sms, stream);
+    launch_route_bwd<1, true>(a, stream);
   else
-    launch_route_bwd<false>(a, dev->num_sms, stream);
+    launch_route_bwd<1, false>(a, stream);
   return launched();
 }
 
-static int run_layout(const LayoutArgs& a, cudaStream_t stream) {
+int64_t fp8_moe_layout_workspace(int64_t T, int64_t top_k, int64_t E) {
+  if (bad_topk(T, top_k) || E < 1 || E > kMaxExperts) return 0;
+  const int64_t n = T * top_k;
+  return n <= kLayoutClusterMax ? 0 : (n + kLayoutChunk - 1) / kLayoutChunk * E;
+}
+
+static int run_layout(LayoutArgs a, cudaStream_t stream) {
+  if (a.n <= kLayoutClusterMax) a.chunk_counts = nullptr;  // not needed
+  if (a.n > kLayoutClusterMax && !a.chunk_counts) return FP8Q_ERR_NULL;
+  if (!aligned(a.chunk_counts, 4)) return FP8Q_ERR_ALIGN;
   DeviceInfo* dev = nullptr;
   int rc = device_info(&dev);
   if (rc) return rc;
+  if (a.n > kLayoutClusterMax) {
+    const unsigned chunks = static_cast<unsigned>((a.n + kLayoutChunk - 1) / kLayoutChunk);
+    moe_layout_count_kernel<<<chunks, kLayoutThreads, 0, stream>>>(a.ids, a.n, a.E, a.chunk_counts);
+    rc = launched();
+    if (rc) return rc;
+    moe_layout_kernel<<<chunks, kLayoutThreads, layout_smem(a.E), stream>>>(a);
+    return launched();
+  }
   // one cluster: a CTA per 1024 entries, up to eight
   unsigned ctas = 1;
   while (ctas < kLayoutMaxCtas && static_cast<int64_t>(ctas) * kLayoutThreads < a.n) ctas *= 2;
@@ -933,7 +950,7 @@ static int run_layout(const LayoutArgs& a, cudaStream_t stream) {
 }
 
 int fp8_moe_layout_contiguous(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* slots,
-                              int32_t* m_indices, int32_t* counts, cudaStream_t stream) {
+                              int32_t* m_indices, int32_t* counts, int32_t* workspace, cudaStream_t stream) {
   FP8Q_API_RANGE();
   if (bad_topk(T, top_k) || E < 1 || E > kMaxExperts) return FP8Q_ERR_SHAPE;
   const int64_t n = T * top_k;
@@ -941,11 +958,12 @@ int fp8_moe_layout_contiguous(const int32_t* ids, int64_t T, int64_t top_k, int6
   if (blocks * 128 >= kMaxRows) return FP8Q_ERR_SHAPE;
   if (!counts || (n && (!ids || !slots || !m_indices))) return FP8Q_ERR_NULL;
   if (!aligned(ids, 4) || !aligned(slots, 4) || !aligned(m_indices, 4) || !aligned(counts, 4)) return FP8Q_ERR_ALIGN;
-  return run_layout(LayoutArgs{ids, n, static_cast<int32_t>(E), 0, slots, m_indices, blocks, counts}, stream);
+  return run_layout(LayoutArgs{ids, n, static_cast<int32_t>(E), 0, slots, m_indices, blocks, counts, workspace},
+                    stream);
 }
 
 int fp8_moe_layout_masked(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int64_t cap, int32_t* slots,
-                          int32_t* masked_m, cudaStream_t stream) {
+                          int32_t* masked_m, int32_t* workspace, cudaStream_t stream) {
   FP8Q_API_RANGE();
   if (bad_topk(T, top_k) || E < 1 || E > kMaxExperts || cap < 128 || cap % 128 || cap >= kMaxRows ||
       E * cap >= kMaxRows || T * top_k >= kMaxRows)
@@ -953,7 +971,7 @@ int fp8_moe_layout_masked(const int32_t* ids, int64_t T, int64_t top_k, int64_t 
   const int64_t n = T * top_k;
   if (!masked_m || (n && (!ids || !slots))) return FP8Q_ERR_NULL;
   if (!aligned(ids, 4) || !aligned(slots, 4) || !aligned(masked_m, 4)) return FP8Q_ERR_ALIGN;
-  return run_layout(LayoutArgs{ids, n, static_cast<int32_t>(E), cap, slots, nullptr, 0, masked_m}, stream);
+  return run_layout(LayoutArgs{ids, n, static_cast<int32_t>(E), cap, slots, nullptr, 0, masked_m, workspace}, stream);
 }
 
 int fp8_moe_dispatch_1x128(const void* x_bf16, int64_t T, int64_t D, const int32_t* slots, int64_t top_k, int64_t rows,

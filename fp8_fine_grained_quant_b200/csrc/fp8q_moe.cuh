@@ -524,8 +524,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_f64_kernel(RouteAr
 //
 // One warp per token.  The chosen experts' values are scattered into a row of
 // shared memory and read back in expert order; only the dense form reads the
-// whole row of logits, once, into registers.  Warps walk the rows at a stride of
-// the grid.
+// whole row of logits, once, into registers.
 // ---------------------------------------------------------------------------
 struct RouteBwdArgs {
   const void* logits;
@@ -544,85 +543,82 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_bwd_kernel(RouteBw
   extern __shared__ float route_grad[];  // [kRouteWarps][E]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
+  if (t >= a.T) return;
   float* d = route_grad + static_cast<int64_t>(warp) * E;
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
     if (i * 32 + lane < E) d[i * 32 + lane] = 0.0f;
+  const void* row = logits_row<kBf16>(a.logits, t, E);
+  float x[kDense ? VPL : 1];
+  if constexpr (kDense) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) x[i] = i * 32 + lane < E ? load_logit<kBf16>(row, i * 32 + lane) : neg_inf_f32();
+  }
+  int id = lane < a.top_k ? __ldg(a.ids + t * a.top_k + lane) : -1;
+  if (id >= E) id = -1;
+  float g = 0.0f, l = neg_inf_f32();
+  if (id >= 0) {
+    g = __ldg(a.dweights + t * a.top_k + lane);
+    if constexpr (!kDense) l = load_logit<kBf16>(row, id);
+  }
+  // dense: p is 0 where the logit is -inf, so its gradient counts for nothing
+  const bool has = id >= 0 && (kDense || l > neg_inf_f32());
+  float v = g;  // dense: the gradient of p; else of the logit
+  if constexpr (!kDense) {
+    const float not_p = a.sigmoid ? 1.0f / (1.0f + expf(l)) : 1.0f;
+    if (a.renorm) {
+      const float r = route_weight(l, has, a.sigmoid, true, 1.0f, 0.0f, 1.0f);
+      const float mean = warp_sum(has ? g * r : 0.0f);
+      v = a.scale * r * (g - mean) * not_p;
+    } else {
+      v = a.scale * g * (1.0f / (1.0f + expf(-l))) * not_p;
+    }
+  }
+  if (!has) v = 0.0f;
+  // an id that appears more than once: the sum, in place order
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, has ? id : -1 - lane);
+  if (__any_sync(0xFFFFFFFFu, __popc(same) > 1)) {
+    float total = 0.0f;
+    for (int j = 0; j < a.top_k; ++j) {
+      const float o = __shfl_sync(0xFFFFFFFFu, v, j);
+      if ((same >> j) & 1u) total += o;
+    }
+    v = total;
+  }
+  __syncwarp();  // the row is zero
+  if (has) d[id] = v;
   __syncwarp();
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp; t < a.T; t += step) {
-    const void* row = logits_row<kBf16>(a.logits, t, E);
-    float x[kDense ? VPL : 1];
-    if constexpr (kDense) {
+  float o[VPL];
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) x[i] = i * 32 + lane < E ? load_logit<kBf16>(row, i * 32 + lane) : neg_inf_f32();
-    }
-    int id = lane < a.top_k ? __ldg(a.ids + t * a.top_k + lane) : -1;
-    if (id >= E) id = -1;
-    float g = 0.0f, l = neg_inf_f32();
-    if (id >= 0) {
-      g = __ldg(a.dweights + t * a.top_k + lane);
-      l = load_logit<kBf16>(row, id);
-    }
-    const bool has = id >= 0 && l > neg_inf_f32();
-    float v = g;  // dense: the gradient of p; else of the logit
-    if constexpr (!kDense) {
-      const float not_p = a.sigmoid ? 1.0f / (1.0f + expf(l)) : 1.0f;
-      if (a.renorm) {
-        const float r = route_weight(l, has, a.sigmoid, true, 1.0f, 0.0f, 1.0f);
-        const float mean = warp_sum(has ? g * r : 0.0f);
-        v = a.scale * r * (g - mean) * not_p;
-      } else {
-        v = a.scale * g * (1.0f / (1.0f + expf(-l))) * not_p;
-      }
-    }
-    if (!has) v = 0.0f;
-    // an id that appears more than once: the sum, in place order
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, has ? id : -1 - lane);
-    if (__any_sync(0xFFFFFFFFu, __popc(same) > 1)) {
-      float total = 0.0f;
-      for (int j = 0; j < a.top_k; ++j) {
-        const float o = __shfl_sync(0xFFFFFFFFu, v, j);
-        if ((same >> j) & 1u) total += o;
-      }
-      v = total;
-    }
-    if (has) d[id] = v;
-    __syncwarp();
-    float o[VPL];
+  for (int i = 0; i < VPL; ++i) o[i] = i * 32 + lane < E ? d[i * 32 + lane] : 0.0f;
+  if constexpr (kDense) {
+    float m = neg_inf_f32();
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) o[i] = i * 32 + lane < E ? d[i * 32 + lane] : 0.0f;
-    __syncwarp();
-    if (has) d[id] = 0.0f;  // for the next row
-    __syncwarp();
-    if constexpr (kDense) {
-      float m = neg_inf_f32();
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
-      m = value_of(redux_max(key_of(m)));  // of logits without NaN
-      float sum = 0.0f, dot = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        x[i] = x[i] > neg_inf_f32() ? expf(x[i] - m) : 0.0f;
-        sum += x[i];
-        dot = fmaf(x[i], o[i], dot);
-      }
-      sum = warp_sum(sum);
-      dot = warp_sum(dot);
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-      const float mean = dot * inv;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) o[i] = a.scale * (x[i] * inv) * (o[i] - mean);
-    }
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
+    m = value_of(redux_max(key_of(m)));  // of logits without NaN
+    float sum = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = i * 32 + lane;
-      if (e < E) {
-        if constexpr (kBf16)
-          static_cast<__nv_bfloat16*>(a.dlogits)[t * E + e] = __float2bfloat16_rn(o[i]);
-        else
-          static_cast<float*>(a.dlogits)[t * E + e] = o[i];
-      }
+      x[i] = x[i] > neg_inf_f32() ? expf(x[i] - m) : 0.0f;
+      sum += x[i];
+      dot = fmaf(x[i], o[i], dot);
+    }
+    sum = warp_sum(sum);
+    dot = warp_sum(dot);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float mean = dot * inv;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) o[i] = a.scale * (x[i] * inv) * (o[i] - mean);
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = i * 32 + lane;
+    if (e < E) {
+      if constexpr (kBf16)
+        static_cast<__nv_bfloat16*>(a.dlogits)[t * E + e] = __float2bfloat16_rn(o[i]);
+      else
+        static_cast<float*>(a.dlogits)[t * E + e] = o[i];
     }
   }
 }
@@ -637,11 +633,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_bwd_kernel(RouteBw
 //
 // One cluster of up to eight CTAs (1024 threads each) takes all entries; every
 // warp owns one run of consecutive entries.  It counts its run's experts into
-// its own row of a shared table (__match_any groups equal ids of 32 entries, so
-// no two lanes touch one counter), the table's columns are turned into exclusive
-// prefixes over the warps, the CTAs' totals are read from one another's shared
-// memory, and the warps walk their runs once more, handing out ranks.  One
-// launch, no workspace, no atomics, and the entries are read twice.
+// its own row of a shared table (the lanes of 32 entries with equal ids find
+// one another by a vote per bit of the id, so no two lanes touch one counter),
+// the table's columns are turned into exclusive prefixes over the warps, the
+// CTAs' totals are read from one another's shared memory, and the warps hand out
+// ranks, from registers where a run is short.  One launch and no atomics.  For
+// many entries a launch before it counts the experts of each chunk into a
+// workspace, and the CTAs of this one, no cluster, sum those.
 // ---------------------------------------------------------------------------
 struct LayoutArgs {
   const int32_t* ids;
@@ -652,13 +650,51 @@ struct LayoutArgs {
   int32_t* m_indices; // contiguous: [blocks]
   int64_t blocks;
   int32_t* counts;    // contiguous: entries of each expert; masked: min(entries, cap)
+  int32_t* chunk_counts;  // [CTAs][E]: the first launch's counts; null: one cluster
 };
+
+// Above this many entries eight SMs are too few for them: the layout takes two
+// launches, a CTA per kLayoutChunk entries, and a workspace.
+constexpr int64_t kLayoutClusterMax = 32768;
+constexpr int kLayoutChunk = 4096;
 
 constexpr int kLayoutThreads = 1024;
 constexpr int kLayoutWarps = kLayoutThreads / 32;
 constexpr int kLayoutMaxCtas = 8;  // the portable cluster size
 constexpr int kLayoutAhead = 4;    // groups of 32 entries loaded together
 constexpr int layout_smem(int E) { return kLayoutWarps * E * 4; }
+
+// The lanes that hold the same id; `bits` covers every id and -1.
+__device__ __forceinline__ uint32_t same_lanes(int e, int bits) {
+  uint32_t same = 0xFFFFFFFFu;
+  for (int b = 0; b < bits; ++b) {
+    const bool set = (e >> b) & 1;
+    const uint32_t v = __ballot_sync(0xFFFFFFFFu, set);
+    same &= set ? v : ~v;
+  }
+  return same;
+}
+
+// First launch of a large layout: the entries of each expert in each chunk
+// (integer shared-memory atomics: their order does not change a count).
+__global__ void __launch_bounds__(kLayoutThreads) moe_layout_count_kernel(const int32_t* __restrict__ ids, int64_t n,
+                                                                          int32_t E, int32_t* __restrict__ counts) {
+  __shared__ int32_t hist[kMaxExperts];
+  const int tid = threadIdx.x;
+  hist[tid] = 0;
+  __syncthreads();
+  int e[kLayoutChunk / kLayoutThreads];
+#pragma unroll
+  for (int k = 0; k < kLayoutChunk / kLayoutThreads; ++k) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kLayoutChunk + k * kLayoutThreads + tid;
+    e[k] = i < n ? __ldg(ids + i) : -1;
+  }
+#pragma unroll
+  for (int k = 0; k < kLayoutChunk / kLayoutThreads; ++k)
+    if (static_cast<uint32_t>(e[k]) < static_cast<uint32_t>(E)) atomicAdd(&hist[e[k]], 1);
+  __syncthreads();
+  if (tid < E) counts[static_cast<int64_t>(blockIdx.x) * E + tid] = hist[tid];
+}
 
 __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(LayoutArgs a) {
   extern __shared__ int32_t layout_table[];  // [kLayoutWarps][E]
@@ -668,52 +704,79 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(LayoutArgs a
   __shared__ int32_t warp_total[kLayoutWarps];
   const auto cluster = cooperative_groups::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int E = a.E;
+  const int E = a.E, bits = 33 - __clz(E);  // the ids below E, and a bit that only -1 has
   int32_t* mine = layout_table + warp * E;
-  // groups of 32 entries of a warp, and its first entry
+  // groups of 32 entries of a warp, its first entry, and the CTA's warps that have any
   const int64_t per_cta = kLayoutWarps * 32 * static_cast<int64_t>(gridDim.x);
   const int64_t groups = (a.n + per_cta - 1) / per_cta;
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * kLayoutWarps + warp) * groups * 32 + lane;
+  const int64_t left = a.n - static_cast<int64_t>(blockIdx.x) * kLayoutWarps * groups * 32;
+  const int warps = left <= 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(kLayoutWarps),
+                                                         (left + groups * 32 - 1) / (groups * 32)));
   auto expert = [&](int64_t g) {
     const int64_t i = first + g * 32;
     const int e = g < groups && i < a.n ? __ldg(a.ids + i) : -1;
     return static_cast<uint32_t>(e) < static_cast<uint32_t>(E) ? e : -1;
   };
-  for (int i = tid; i < kLayoutWarps * E; i += kLayoutThreads) layout_table[i] = 0;
+  int e[kLayoutAhead];
+  uint32_t same[kLayoutAhead];
+#pragma unroll
+  for (int k = 0; k < kLayoutAhead; ++k) e[k] = expert(k);
+  for (int i = tid; i < warps * E; i += kLayoutThreads) layout_table[i] = 0;
   __syncthreads();
-  for (int64_t g = 0; g < groups; g += kLayoutAhead) {
-    int e[kLayoutAhead];
+  if (warp < warps) {
+    for (int64_t g = 0; g < groups; g += kLayoutAhead) {
+      if (g > 0) {
 #pragma unroll
-    for (int k = 0; k < kLayoutAhead; ++k) e[k] = expert(g + k);
+        for (int k = 0; k < kLayoutAhead; ++k) e[k] = expert(g + k);
+      }
 #pragma unroll
-    for (int k = 0; k < kLayoutAhead; ++k) {
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e[k]);
-      if (e[k] >= 0 && lane == __ffs(same) - 1) mine[e[k]] += __popc(same);
-      __syncwarp();
+      for (int k = 0; k < kLayoutAhead; ++k) same[k] = g + k < groups ? same_lanes(e[k], bits) : 0u;
+#pragma unroll
+      for (int k = 0; k < kLayoutAhead; ++k) {
+        if (e[k] >= 0 && lane == __ffs(same[k]) - 1) mine[e[k]] += __popc(same[k]);
+        __syncwarp();
+      }
     }
   }
   __syncthreads();
+  int32_t count = 0, ahead = 0;
   if (tid < E) {
-    int32_t sum = 0;
 #pragma unroll 8
-    for (int w = 0; w < kLayoutWarps; ++w) {
+    for (int w = 0; w < warps; ++w) {
       const int32_t c = layout_table[w * E + tid];
-      layout_table[w * E + tid] = sum;
-      sum += c;
+      layout_table[w * E + tid] = count;
+      count += c;
     }
-    hist[tid] = sum;
+    hist[tid] = count;
   }
-  cluster.sync();
-  int32_t ahead = 0, count = 0;
-  if (tid < E) {
-    for (unsigned r = 0; r < gridDim.x; ++r) {
-      const int32_t h = *cluster.map_shared_rank(&hist[tid], r);
-      if (r < blockIdx.x) ahead += h;
-      count += h;
+  if (a.chunk_counts != nullptr) {
+    if (tid < E) {
+      count = 0;
+#pragma unroll 8
+      for (unsigned r = 0; r < gridDim.x; ++r) {
+        const int32_t h = __ldg(a.chunk_counts + static_cast<int64_t>(r) * E + tid);
+        if (r < blockIdx.x) ahead += h;
+        count += h;
+      }
     }
-    before[tid] = ahead;
+  } else if (gridDim.x > 1) {
+    cluster.sync();
+    if (tid < E) {
+      int32_t h[kLayoutMaxCtas];
+#pragma unroll
+      for (unsigned r = 0; r < kLayoutMaxCtas; ++r)
+        h[r] = r < gridDim.x ? *cluster.map_shared_rank(&hist[tid], r) : 0;
+      count = 0;
+#pragma unroll
+      for (unsigned r = 0; r < kLayoutMaxCtas; ++r) {
+        if (r < blockIdx.x) ahead += h[r];
+        count += h[r];
+      }
+    }
+    cluster.sync();  // no CTA may end while another reads its counts
   }
-  cluster.sync();  // no CTA may end while another reads its counts
+  if (tid < E) before[tid] = ahead;
   // exclusive prefix of the experts' blocks of 128 rows
   const int size = (count + 127) >> 7;
   int incl = size;
@@ -740,25 +803,29 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(LayoutArgs a
   if (blockIdx.x == 0 && tid < E)
     a.counts[tid] = a.cap > 0 && count > a.cap ? static_cast<int32_t>(a.cap) : count;
   __syncthreads();
-  for (int64_t g = 0; g < groups; g += kLayoutAhead) {
-    int e[kLayoutAhead];
+  if (warp < warps) {
+    for (int64_t g = 0; g < groups; g += kLayoutAhead) {
+      if (groups > kLayoutAhead) {  // else still in registers
 #pragma unroll
-    for (int k = 0; k < kLayoutAhead; ++k) e[k] = expert(g + k);
+        for (int k = 0; k < kLayoutAhead; ++k) e[k] = expert(g + k);
 #pragma unroll
-    for (int k = 0; k < kLayoutAhead; ++k) {
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e[k]);
-      int64_t slot = -1;
-      if (e[k] >= 0) {
-        const int64_t r = static_cast<int64_t>(before[e[k]]) + mine[e[k]] + __popc(same & ((1u << lane) - 1u));
-        if (a.cap > 0)
-          slot = r < a.cap ? e[k] * a.cap + r : -1;
-        else
-          slot = static_cast<int64_t>(start[e[k]]) * 128 + r;
+        for (int k = 0; k < kLayoutAhead; ++k) same[k] = g + k < groups ? same_lanes(e[k], bits) : 0u;
       }
-      __syncwarp();
-      if (e[k] >= 0 && lane == __ffs(same) - 1) mine[e[k]] += __popc(same);
-      __syncwarp();
-      if (g + k < groups && first + (g + k) * 32 < a.n) a.slots[first + (g + k) * 32] = static_cast<int32_t>(slot);
+#pragma unroll
+      for (int k = 0; k < kLayoutAhead; ++k) {
+        int64_t slot = -1;
+        if (e[k] >= 0) {
+          const int64_t r = static_cast<int64_t>(before[e[k]]) + mine[e[k]] + __popc(same[k] & ((1u << lane) - 1u));
+          if (a.cap > 0)
+            slot = r < a.cap ? e[k] * a.cap + r : -1;
+          else
+            slot = static_cast<int64_t>(start[e[k]]) * 128 + r;
+        }
+        __syncwarp();
+        if (e[k] >= 0 && lane == __ffs(same[k]) - 1) mine[e[k]] += __popc(same[k]);
+        __syncwarp();
+        if (g + k < groups && first + (g + k) * 32 < a.n) a.slots[first + (g + k) * 32] = static_cast<int32_t>(slot);
+      }
     }
   }
   if (a.cap == 0) {

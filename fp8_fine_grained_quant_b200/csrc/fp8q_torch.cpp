@@ -10,6 +10,7 @@
 #include <torch/extension.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -93,7 +94,7 @@ struct Place {
 
 template <typename T = void>
 T* ptr(const Tensor& t) {
-  return static_cast<T*>(t.data_ptr());
+  return t.defined() ? static_cast<T*>(t.data_ptr()) : nullptr;
 }
 template <typename T = void>
 T* ptr(const Opt& t) {
@@ -111,6 +112,18 @@ struct On {
     else
       stream = reinterpret_cast<cudaStream_t>(
           (py::hasattr(s, "cuda_stream") ? s.attr("cuda_stream") : s).cast<uintptr_t>());
+  }
+  // n int32 of scratch for work on this stream only (an undefined tensor for none).  The allocator may hand the
+  // memory out again once it is dropped: to work queued on the device's current stream, or, where the call runs on
+  // another one, after that stream has passed this point.
+  Tensor scratch(int64_t n) const {
+    if (n == 0) return Tensor();
+    Tensor t = at::detail::empty_cuda({n}, at::kInt, guard.current_device(), std::nullopt);
+    const auto index = guard.current_device().index();
+    if (stream != c10::cuda::getCurrentCUDAStream(index).stream())
+      c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(),
+                                                    c10::cuda::getStreamFromExternal(stream, index));
+    return t;
   }
   Tensor fresh(const Opt& given, at::IntArrayRef shape, at::ScalarType type) const {
     return given ? *given : at::Tensor(at::detail::empty_cuda(shape, type, guard.current_device(), std::nullopt));
@@ -210,8 +223,9 @@ py::tuple layout_contiguous(const Tensor& ids, int64_t E, const Opt& slots, cons
   const On on(p, stream);
   const Tensor s = on.fresh(slots, {T, top_k}, at::kInt), m = on.fresh(m_indices, {B}, at::kInt),
                c = on.fresh(counts, {E}, at::kInt);
+  const Tensor w = on.scratch(fp8_moe_layout_workspace(T, top_k, E));
   check(fp8_moe_layout_contiguous(ptr<int32_t>(ids), T, top_k, E, ptr<int32_t>(s), ptr<int32_t>(m), ptr<int32_t>(c),
-                                  on.stream),
+                                  ptr<int32_t>(w), on.stream),
         "fp8_moe_layout_contiguous");
   return py::make_tuple(s, m, c);
 }
@@ -230,7 +244,9 @@ py::tuple layout_masked(const Tensor& ids, int64_t E, int64_t cap, const Opt& sl
   p.add(masked_m, "masked_m");
   const On on(p, stream);
   const Tensor s = on.fresh(slots, {T, top_k}, at::kInt), m = on.fresh(masked_m, {E}, at::kInt);
-  check(fp8_moe_layout_masked(ptr<int32_t>(ids), T, top_k, E, cap, ptr<int32_t>(s), ptr<int32_t>(m), on.stream),
+  const Tensor w = on.scratch(fp8_moe_layout_workspace(T, top_k, E));
+  check(fp8_moe_layout_masked(ptr<int32_t>(ids), T, top_k, E, cap, ptr<int32_t>(s), ptr<int32_t>(m), ptr<int32_t>(w),
+                              on.stream),
         "fp8_moe_layout_masked");
   return py::make_tuple(s, m);
 }

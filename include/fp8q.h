@@ -358,13 +358,18 @@ FP8Q_API int fp8_moe_route_bwd(const void* logits, int logits_bf16, int64_t T, i
  *   counts    : [E] int32, written: entries of each expert.
  * Masked: row expert * cap + rank; entries whose rank reaches cap get -1.
  *   masked_m  : [E] int32, written: min(entries, cap) of each expert.
+ *   workspace : scratch of fp8_moe_layout_workspace(T, top_k, E) int32 (0 for up
+ *               to 32768 entries: may be NULL).  Its contents before the call do
+ *               not matter; calls that may run at the same time need their own.
  * 1 <= E <= 1024, 1 <= top_k <= 32, cap a positive multiple of 128, rows below
  * 2^31.  With T == 0 the counts are still written.  Pointers 4-byte aligned.
  */
 FP8Q_API int fp8_moe_layout_contiguous(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int32_t* slots,
-                                       int32_t* m_indices, int32_t* counts, cudaStream_t stream);
+                                       int32_t* m_indices, int32_t* counts, int32_t* workspace,
+                                       cudaStream_t stream);
 FP8Q_API int fp8_moe_layout_masked(const int32_t* ids, int64_t T, int64_t top_k, int64_t E, int64_t cap,
-                                   int32_t* slots, int32_t* masked_m, cudaStream_t stream);
+                                   int32_t* slots, int32_t* masked_m, int32_t* workspace, cudaStream_t stream);
+FP8Q_API int64_t fp8_moe_layout_workspace(int64_t T, int64_t top_k, int64_t E);
 
 /*
  * Dispatch of tokens to expert rows, fused with the 1x128 quantization: row

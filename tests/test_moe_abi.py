@@ -50,18 +50,20 @@ CASES = [
     ("fp8_moe_route_bwd", (A16, 0, 0, 8, None, None, 0, 2, 1, 1.0, None, None), fq.OK),
     ("fp8_moe_route_bwd", (A16, 0, 4, 8, None, A16, 0, 2, 1, 1.0, A16, None), fq.ERR_NULL),
     ("fp8_moe_route_bwd", (A16, 0, 4, 8, A16, A16, 0, 2, 1, 1.0, A2, None), fq.ERR_ALIGN),
-    ("fp8_moe_layout_contiguous", (A16, 4, 0, 8, A16, A16, A16, None), fq.ERR_SHAPE),
-    ("fp8_moe_layout_contiguous", (A16, 4, 2, 1025, A16, A16, A16, None), fq.ERR_SHAPE),
-    ("fp8_moe_layout_contiguous", (A16, BIG - 1, 2, 8, A16, A16, A16, None), fq.ERR_SHAPE),   # 2^32 rows
-    ("fp8_moe_layout_contiguous", (A16, 4, 2, 8, A16, A16, None, None), fq.ERR_NULL),
-    ("fp8_moe_layout_contiguous", (A16, 4, 2, 8, None, A16, A16, None), fq.ERR_NULL),
-    ("fp8_moe_layout_contiguous", (A16, 0, 2, 8, None, None, None, None), fq.ERR_NULL),       # counts are written
-    ("fp8_moe_layout_contiguous", (A1, 4, 2, 8, A16, A16, A16, None), fq.ERR_ALIGN),
-    ("fp8_moe_layout_masked", (A16, 4, 2, 8, 100, A16, A16, None), fq.ERR_SHAPE),
-    ("fp8_moe_layout_masked", (A16, 4, 2, 8, 0, A16, A16, None), fq.ERR_SHAPE),
-    ("fp8_moe_layout_masked", (A16, 4, 2, 1024, 1 << 21, A16, A16, None), fq.ERR_SHAPE),      # E * cap = 2^31
-    ("fp8_moe_layout_masked", (A16, 4, 2, 8, 128, A16, None, None), fq.ERR_NULL),
-    ("fp8_moe_layout_masked", (A16, 4, 2, 8, 128, A1, A16, None), fq.ERR_ALIGN),
+    ("fp8_moe_layout_contiguous", (A16, 4, 0, 8, A16, A16, A16, A16, None), fq.ERR_SHAPE),
+    ("fp8_moe_layout_contiguous", (A16, 4, 2, 1025, A16, A16, A16, A16, None), fq.ERR_SHAPE),
+    ("fp8_moe_layout_contiguous", (A16, BIG - 1, 2, 8, A16, A16, A16, A16, None), fq.ERR_SHAPE),   # 2^32 rows
+    ("fp8_moe_layout_contiguous", (A16, 4, 2, 8, A16, A16, None, A16, None), fq.ERR_NULL),
+    ("fp8_moe_layout_contiguous", (A16, 4, 2, 8, None, A16, A16, A16, None), fq.ERR_NULL),
+    ("fp8_moe_layout_contiguous", (A16, 0, 2, 8, None, None, None, A16, None), fq.ERR_NULL),       # counts are written
+    ("fp8_moe_layout_contiguous", (A1, 4, 2, 8, A16, A16, A16, A16, None), fq.ERR_ALIGN),
+    ("fp8_moe_layout_masked", (A16, 4, 2, 8, 100, A16, A16, A16, None), fq.ERR_SHAPE),
+    ("fp8_moe_layout_masked", (A16, 4, 2, 8, 0, A16, A16, A16, None), fq.ERR_SHAPE),
+    ("fp8_moe_layout_masked", (A16, 4, 2, 1024, 1 << 21, A16, A16, A16, None), fq.ERR_SHAPE),      # E * cap = 2^31
+    ("fp8_moe_layout_masked", (A16, 4, 2, 8, 128, A16, None, A16, None), fq.ERR_NULL),
+    ("fp8_moe_layout_masked", (A16, 4, 2, 8, 128, A1, A16, A16, None), fq.ERR_ALIGN),
+    ("fp8_moe_layout_masked", (A16, 10000, 8, 8, 128, A16, A16, None, None), fq.ERR_NULL),    # needs a workspace
+    ("fp8_moe_layout_contiguous", (A16, 10000, 8, 8, A16, A16, A16, A1, None), fq.ERR_ALIGN),
     ("fp8_moe_dispatch_1x128", (A16, 4, 100, A16, 2, 256, None, None, 0, A16, A16, None), fq.ERR_SHAPE),
     ("fp8_moe_dispatch_1x128", (A16, 4, 128, A16, 2, -1, None, None, 0, A16, A16, None), fq.ERR_SHAPE),
     ("fp8_moe_dispatch_1x128", (A16, BIG - 1, 256, A16, 2, 256, None, None, 0, A16, A16, None), fq.ERR_SHAPE),
@@ -179,6 +181,13 @@ def test_route_bwd_arguments():
         fq.fp8_moe_route_bwd(lg(), ids.long(), g)
     with pytest.raises(ValueError, match="CUDA tensor"):
         fq.fp8_moe_route_bwd(lg(), ids, g)
+
+
+def test_layout_workspace_size():
+    ws = fq.lib().fp8_moe_layout_workspace
+    assert ws(4096, 8, 32) == 0                       # one cluster
+    assert ws(4097, 8, 32) == 9 * 32                  # 32776 entries: nine chunks of 4096
+    assert ws(-1, 8, 32) == ws(4097, 33, 32) == ws(4097, 8, 1025) == 0
 
 
 def test_layout_arguments():

@@ -203,7 +203,8 @@ def _ids(rng, T, E, k, idle=0.1):
 
 
 LAYOUTS = [(0, 8, 2), (1, 1, 1), (1, 32, 8), (5, 3, 2), (128, 1, 1), (129, 2, 1), (1000, 32, 8), (4097, 7, 3),
-           (513, 1024, 2), (3000, 256, 8), (40, 4, 32), (2048, 60, 5)]
+           (513, 1024, 2), (3000, 256, 8), (40, 4, 32), (2048, 60, 5), (4096, 32, 8), (4097, 32, 8),
+           (32769, 1024, 1), (9000, 300, 6)]
 
 
 @pytest.mark.parametrize("T,E,k", LAYOUTS)
@@ -234,6 +235,25 @@ def test_layout_of_many_entries(dev):
         os_, om, oc = moe.layout_contiguous(ids, 200)
         assert np.array_equal(slots.cpu().numpy(), os_) and np.array_equal(m.cpu().numpy(), om)
         assert np.array_equal(counts.cpu().numpy(), oc)
+
+
+def test_large_layout_on_another_stream(dev):
+    """The workspace of a large layout belongs to the stream the call names: two
+    streams at once, each with its own entries, repeated."""
+    rng = np.random.default_rng(4)
+    hosts = [_ids(rng, 6000, 64, 8), _ids(rng, 7000, 64, 8)]
+    devs = [torch.from_numpy(h).to(dev) for h in hosts]
+    side = torch.cuda.Stream(dev)
+    torch.cuda.synchronize(dev)
+    got = []
+    for _ in range(8):
+        got.append([fq.fp8_moe_layout_contiguous(devs[0], 64), fq.fp8_moe_layout_contiguous(devs[1], 64, stream=side)])
+    torch.cuda.synchronize(dev)
+    for pair in got:
+        for host, (slots, m, counts) in zip(hosts, pair):
+            os_, om, oc = moe.layout_contiguous(host, 64)
+            assert np.array_equal(slots.cpu().numpy(), os_) and np.array_equal(m.cpu().numpy(), om)
+            assert np.array_equal(counts.cpu().numpy(), oc)
 
 
 def _bf16(rng, shape, scale=1.0):
