@@ -19,23 +19,25 @@
 
 namespace fp8q {
 
-// ------------------------------------------------------------ exp(-g) for a pair
-// e^x = 2^(x L) with L = log2 e: t = fl(x L), and what t lacks, x L - t =
-// fma(x, L, -t) + x (log2 e - L), enters as a factor 1 + ln 2 times it.  With
-// ex2.approx (2^-22) the result is within 2^-21.9.  For g in [-88, 2^126]: at the
-// lower end 1 / (1 + e) is 0 (flushed), at the upper e is.
-__device__ __forceinline__ uint64_t exp_neg_f32x2(uint64_t g) {
-  constexpr float kL = 1.44269504f;  // nearest FP32 to log2 e, 1.925963e-8 below it
-  const uint64_t t = mul_f32x2(g, pack_f32x2(-kL));
-  // what t lacks, negated: g L + t + g (log2 e - L)
-  uint64_t r = fma_f32x2(g, pack_f32x2(kL), t);
-  r = fma_f32x2(g, pack_f32x2(1.925963e-8f), r);
+// ------------------------------------------------------------ 1 / (1 + exp(-g))
+// For bf16 g in [-88, 2^126], a pair.  With log2 e = H + l, H its first 16 bits:
+// exp(-g) = 2^(-g H) e^(-g l ln 2), where g H is exact (8 bits by 16) and the
+// second factor is 1 - g l ln 2 to (g l ln 2)^2 / 2 <= 2^-23.3.  With ex2.approx
+// (2^-22), the factor's and the sum's roundings (2^-24 each) and rcp.approx.ftz
+// (2^-23): below 5.7e-7.  At -88 the result is 0 (flushed).
+__device__ __forceinline__ uint64_t sigmoid_bf16x2(uint64_t g) {
+  constexpr float kH = 47274.0f / 32768.0f;     // log2 e = 1.44269504089 to 16 bits
+  constexpr float kLowLn2 = 4.8884952e-6f;      // (log2 e - H) ln 2
   float t0, t1, e0, e1;
-  split_f32x2(t, t0, t1);
+  split_f32x2(mul_f32x2(g, pack_f32x2(-kH)), t0, t1);
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
-  const uint64_t e = join_f32x2(e0, e1);
-  return fma_f32x2(e, mul_f32x2(r, pack_f32x2(-0.693147181f)), e);
+  const uint64_t one = pack_f32x2(1.0f);
+  float a, b, x, y;
+  split_f32x2(fma_f32x2(join_f32x2(e0, e1), fma_f32x2(g, pack_f32x2(-kLowLn2), one), one), a, b);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(a));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(b));
+  return join_f32x2(x, y);
 }
 // 1 / (1 + e) by rcp.approx.ftz (1 ulp).
 __device__ __forceinline__ uint64_t rcp_one_plus(uint64_t e) {
@@ -47,10 +49,9 @@ __device__ __forceinline__ uint64_t rcp_one_plus(uint64_t e) {
 }
 
 // h = bf16(silu(g) u), correctly rounded, for the 16 elements of a lane; the
-// same values as swiglu16.  FP32: exp 2^-21.9 (weighted by 1 - p), 1 + e 2^-24,
-// rcp 2^-23, two products 2^-23: below 2^-20.8.  Where h (1 -+ 1.375 * 2^-21),
-// their roundings counted, give one bf16, that is it; elements they leave open
-// (about one in 3000), and those outside [2^-99, 2^119], are evaluated in
+// same values as swiglu16.  FP32: 5.7e-7 from p (above) and 1.2e-7 from two
+// products.  Where h (1 -+ 7.75e-7), whose own roundings are 0.6e-7, give one
+// bf16, that is it; elements they leave open (about one in 2500), and those outside [2^-99, 2^119], are evaluated in
 // double, their words read again at gp and up.  Gates below -88 enter as -88,
 // where h comes out as 0 and is evaluated in double; lanes with a gate above
 // 2^126 (g_max, the lane's largest magnitude) are too.  Returns the largest |h|.
@@ -61,9 +62,9 @@ __device__ __forceinline__ float swiglu16_f32x2(const uint32_t (&gw)[8], const u
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint64_t g = bf16x2_to_f32x2(max_bf16x2(gw[i], 0xC2B0C2B0u)), u = bf16x2_to_f32x2(uw[i]);  // -88
-    const uint64_t h = mul_f32x2(mul_f32x2(g, rcp_one_plus(exp_neg_f32x2(g))), u);
-    hw[i] = bf16x2_from_pair(mul_f32x2(h, pack_f32x2(1.0f - 0x1.6p-21f)));
-    d[i] = hw[i] ^ bf16x2_from_pair(mul_f32x2(h, pack_f32x2(1.0f + 0x1.6p-21f)));
+    const uint64_t h = mul_f32x2(mul_f32x2(g, sigmoid_bf16x2(g)), u);
+    hw[i] = bf16x2_from_pair(mul_f32x2(h, pack_f32x2(1.0f - 0x1.ap-21f)));
+    d[i] = hw[i] ^ bf16x2_from_pair(mul_f32x2(h, pack_f32x2(1.0f + 0x1.ap-21f)));
     any |= d[i];
     const uint32_t m = hw[i] & 0x7FFF7FFFu;
     most = max_bf16x2(most, m);
@@ -113,37 +114,46 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_1x128_kernel(const uint8_t
   const int64_t grp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
   const int64_t ngrp = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 3;
   const uint32_t per_row = static_cast<uint32_t>(inter >> 7);
+  // tile t of h is tile kb of row `row`; a step moves (row, kb) by a constant, with a carry
+  const uint32_t step_row = static_cast<uint32_t>(ngrp) / per_row, step_kb = static_cast<uint32_t>(ngrp) % per_row;
+  uint32_t row = static_cast<uint32_t>(grp) / per_row, kb = static_cast<uint32_t>(grp) % per_row;
   for (int64_t t = grp; (t & ~int64_t(3)) < num_tiles; t += ngrp) {
     const bool valid = t < num_tiles;
-    const uint32_t row = valid ? static_cast<uint32_t>(t) / per_row : 0u;
-    const uint32_t kb = valid ? static_cast<uint32_t>(t) - row * per_row : 0u;
-    const int64_t gate = static_cast<int64_t>(row) * 2 * inter + static_cast<int64_t>(kb) * 128 + sub * 16;
+    const uint64_t gate = static_cast<uint64_t>(row) * (2 * per_row) + kb, up = gate + per_row;  // tiles of c1
     uint32_t gw[8], uw[8], hw[8];
-    float ah = 0.0f, ag = 0.0f, au = 0.0f;
+    float ah = 0.0f;
+    uint32_t agu = 0u;  // largest |gate| (low half) and |up| as bf16
     if (valid) {
-      ld_nc_v8(c1 + gate * 2, gw);
-      ld_nc_v8(c1 + (gate + inter) * 2, uw);
-      ag = abs_max16(gw);
-      au = abs_max16(uw);
-      ah = swiglu16_f32x2(gw, uw, hw, ag, c1 + gate * 2, c1 + (gate + inter) * 2);
+      const uint8_t* gp = c1 + gate * 256 + sub * 32;
+      const uint8_t* upp = c1 + up * 256 + sub * 32;
+      ld_nc_v8(gp, gw);
+      ld_nc_v8(upp, uw);
+      const float ag = abs_max16(gw), au = abs_max16(uw);
+      agu = (__float_as_uint(ag) >> 16) | __float_as_uint(au);
+      ah = swiglu16_f32x2(gw, uw, hw, ag, gp, upp);
     }
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) {
       ah = fmaxf(ah, __shfl_xor_sync(0xFFFFFFFFu, ah, off));
-      ag = fmaxf(ag, __shfl_xor_sync(0xFFFFFFFFu, ag, off));
-      au = fmaxf(au, __shfl_xor_sync(0xFFFFFFFFu, au, off));
+      agu = max_bf16x2(agu, __shfl_xor_sync(0xFFFFFFFFu, agu, off));
     }
     if (valid) {
-      const float s_h = group_scale(ah), s_g = group_scale(ag), s_u = group_scale(au);
+      const float s_h = group_scale(ah), s_g = group_scale(__uint_as_float(agu << 16)),
+                  s_u = group_scale(__uint_as_float(agu & 0xFFFF0000u));
       *reinterpret_cast<uint4*>(qh + t * 128 + sub * 16) = codes16_bf16(hw, s_h);
-      *reinterpret_cast<uint4*>(qc + gate) = codes16_bf16(gw, s_g);
-      *reinterpret_cast<uint4*>(qc + gate + inter) = codes16_bf16(uw, s_u);
+      *reinterpret_cast<uint4*>(qc + gate * 128 + sub * 16) = codes16_bf16(gw, s_g);
+      *reinterpret_cast<uint4*>(qc + up * 128 + sub * 16) = codes16_bf16(uw, s_u);
       if (sub == 0) {
         sh[t] = s_h;
-        const int64_t g = static_cast<int64_t>(row) * 2 * per_row + kb;
-        sc[g] = s_g;
-        sc[g + per_row] = s_u;
+        sc[gate] = s_g;
+        sc[up] = s_u;
       }
+    }
+    row += step_row;
+    kb += step_kb;
+    if (kb >= per_row) {
+      kb -= per_row;
+      ++row;
     }
   }
 }
@@ -193,12 +203,12 @@ __device__ __forceinline__ float abs_max16_f32x2(const uint64_t (&v)[8]) {
   for (int i = 0; i < 8; ++i) {
     float a, b;
     split_f32x2(v[i], a, b);
-    m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+    m = max3_abs(m, a, b);
   }
   return m;
 }
 
-__global__ void __launch_bounds__(256, 3) swiglu_bwd_1x128_kernel(const uint8_t* __restrict__ dh,
+__global__ void __launch_bounds__(256, 4) swiglu_bwd_1x128_kernel(const uint8_t* __restrict__ dh,
                                                                   const uint8_t* __restrict__ qc,
                                                                   const float* __restrict__ sc,
                                                                   uint8_t* __restrict__ dc, uint8_t* __restrict__ q,
@@ -208,20 +218,25 @@ __global__ void __launch_bounds__(256, 3) swiglu_bwd_1x128_kernel(const uint8_t*
   const int64_t grp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
   const int64_t ngrp = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 3;
   const uint32_t per_row = static_cast<uint32_t>(inter >> 7);
+  const uint32_t step_row = static_cast<uint32_t>(ngrp) / per_row, step_kb = static_cast<uint32_t>(ngrp) % per_row;
+  uint32_t row = static_cast<uint32_t>(grp) / per_row, kb = static_cast<uint32_t>(grp) % per_row;
   for (int64_t t = grp; (t & ~int64_t(3)) < num_tiles; t += ngrp) {
     const bool valid = t < num_tiles;
-    const uint32_t row = valid ? static_cast<uint32_t>(t) / per_row : 0u;
-    const uint32_t kb = valid ? static_cast<uint32_t>(t) - row * per_row : 0u;
-    const int64_t gate = static_cast<int64_t>(row) * 2 * inter + static_cast<int64_t>(kb) * 128 + sub * 16;
-    const int64_t si = static_cast<int64_t>(row) * 2 * per_row + kb;
+    const uint64_t gate = static_cast<uint64_t>(row) * (2 * per_row) + kb;  // tile of the gate half
+    row += step_row;
+    kb += step_kb;
+    if (kb >= per_row) {
+      kb -= per_row;
+      ++row;
+    }
     uint64_t dg[8], du[8];
     float ag = 0.0f, au = 0.0f;
     if (valid) {
       uint32_t dw[8];
       ld_nc_v8(dh + t * 256 + sub * 32, dw);
-      const uint4 cg = ld_nc_v4(qc + gate), cu = ld_nc_v4(qc + gate + inter);
+      const uint4 cg = ld_nc_v4(qc + gate * 128 + sub * 16), cu = ld_nc_v4(qc + (gate + per_row) * 128 + sub * 16);
       const uint32_t gc[4] = {cg.x, cg.y, cg.z, cg.w}, uc[4] = {cu.x, cu.y, cu.z, cu.w};
-      const uint64_t s_g = pack_f32x2(__ldg(sc + si)), s_u = pack_f32x2(__ldg(sc + si + per_row));
+      const uint64_t s_g = pack_f32x2(__ldg(sc + gate)), s_u = pack_f32x2(__ldg(sc + gate + per_row));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint64_t g0, g1, u0, u1;
@@ -247,11 +262,11 @@ __global__ void __launch_bounds__(256, 3) swiglu_bwd_1x128_kernel(const uint8_t*
       uint32_t o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = bf16x2_from_pair(d[i]);
-      const int64_t at = gate + half * inter;
-      *reinterpret_cast<uint4*>(dc + at * 2) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(dc + at * 2 + 16) = make_uint4(o[4], o[5], o[6], o[7]);
-      *reinterpret_cast<uint4*>(q + at) = codes16_f32(d, sv);
-      if (sub == 0) s[si + half * per_row] = sv;
+      const uint64_t at = gate + half * per_row;
+      *reinterpret_cast<uint4*>(dc + at * 256 + sub * 32) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(dc + at * 256 + sub * 32 + 16) = make_uint4(o[4], o[5], o[6], o[7]);
+      *reinterpret_cast<uint4*>(q + at * 128 + sub * 16) = codes16_f32(d, sv);
+      if (sub == 0) s[at] = sv;
     }
   }
 }
@@ -305,17 +320,22 @@ __global__ void __launch_bounds__(128, 5) ckpt_128x1_t_kernel(const uint8_t* __r
   uint64_t v[8][4];  // [token][channel pair]
   float m[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const uint64_t s2 = pack_f32x2(sr[r]);
-    e4m3x4_to_f32x2(c[r].x, v[r][0], v[r][1]);
-    e4m3x4_to_f32x2(c[r].y, v[r][2], v[r][3]);
+  for (int r = 0; r < 8; r += 2) {
+#pragma unroll
+    for (int k = r; k < r + 2; ++k) {
+      const uint64_t s2 = pack_f32x2(sr[k]);
+      e4m3x4_to_f32x2(c[k].x, v[k][0], v[k][1]);
+      e4m3x4_to_f32x2(c[k].y, v[k][2], v[k][3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[k][i] = mul_f32x2(v[k][i], s2);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[r][i] = mul_f32x2(v[r][i], s2);
-      float a, b;
+      float a, b, x, y;
       split_f32x2(v[r][i], a, b);
-      m[2 * i] = fmaxf(m[2 * i], fabsf(a));
-      m[2 * i + 1] = fmaxf(m[2 * i + 1], fabsf(b));
+      split_f32x2(v[r + 1][i], x, y);
+      m[2 * i] = max3_abs(m[2 * i], a, x);
+      m[2 * i + 1] = max3_abs(m[2 * i + 1], b, y);
     }
   }
   // lanes l, l ^ 8, l ^ 16 and l ^ 24 hold the same channels (the warp's four token groups)

@@ -192,22 +192,21 @@ __device__ __noinline__ int route_choose_f64(const RouteArgs& a, const void* row
   return mine;
 }
 
-// Order-preserving map of FP32 to uint32 and back; 0 is below every finite
-// value and stands for "never chosen".
-__device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t b = __float_as_uint(v);
-  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+// Largest and smallest value of a warp, one instruction each.
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
-__device__ __forceinline__ float value_of(uint32_t k) {
-  return __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
+__device__ __forceinline__ float redux_min(float v) {
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
-
-__device__ __forceinline__ uint32_t redux_max(uint32_t v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
-__device__ __forceinline__ uint32_t redux_min(uint32_t v) { return __reduce_min_sync(0xFFFFFFFFu, v); }
 
 // N values in descending order, by an odd-even merge network (N a power of two).
 template <int N>
-__device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
+__device__ __forceinline__ void sort_descending(float (&v)[N]) {
 #pragma unroll
   for (int p = 1; p < N; p <<= 1) {
 #pragma unroll
@@ -215,9 +214,9 @@ __device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         if (i + q < N && i >= q % p && (i - q % p) / q % 2 == 0 && i / (2 * p) == (i + q) / (2 * p)) {
-          const uint32_t x = v[i], y = v[i + q < N ? i + q : i];
-          v[i] = max(x, y);
-          v[i + q < N ? i + q : i] = min(x, y);
+          const float x = v[i], y = v[i + q < N ? i + q : i];
+          v[i] = fmaxf(x, y);
+          v[i + q < N ? i + q : i] = fminf(x, y);
         }
       }
     }
@@ -345,15 +344,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
     share_values<VPL, kBf16>(raw, sp.vector, l);
     if (t + step < a.T)
       load_share<VPL, kBf16>(logits_row<kBf16>(a.logits, t + step, a.E), base, count, sp.vector, raw);
-    if (!kSigmoid || !biased) {  // a sigmoid of +inf needs no bound
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) l[i] = l[i] > neg_inf_f32() ? fminf(l[i], FLT_MAX) : neg_inf_f32();
-    }
+    for (int i = 0; i < VPL; ++i) l[i] = fminf(fmaxf(l[i], neg_inf_f32()), FLT_MAX);  // NaN to -inf
     float row_max = neg_inf_f32(), row_sum = 0.0f;
     if (stats) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) row_max = fmaxf(row_max, l[i]);
-      row_max = warp_max(row_max);
+      row_max = redux_max(row_max);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         if (l[i] > neg_inf_f32()) row_sum += a.renorm ? exp_approx(l[i] - row_max) : expf(l[i] - row_max);
@@ -365,16 +362,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
       return kSigmoid ? rcp_approx(1.0f + exp_approx(-x)) : exp_approx(x - row_max) * inv_sum;
     };
 
-    // keys: the logits (-0 as +0), or score + bias
-    uint32_t key[VPL], s[VPL];
+    // keys: the logits (-0 as +0), or score + bias; -inf: never chosen
+    float key[VPL], s[VPL];
     if (!biased) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = l[i] > neg_inf_f32() ? key_of(l[i] + 0.0f) : 0u;
+      for (int i = 0; i < VPL; ++i) key[i] = l[i] + 0.0f;
     } else {
+      float least = l[0];
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        const float k = score(l[i]) + bias[i];
-        key[i] = l[i] > neg_inf_f32() && k > neg_inf_f32() ? key_of(k) : 0u;
+        key[i] = score(l[i]) + bias[i];
+        least = fminf(least, l[i]);
+      }
+      if (least == neg_inf_f32()) {  // the sigmoid of -inf is 0, of a masked row's softmax NaN
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = l[i] == neg_inf_f32() ? neg_inf_f32() : key[i];
       }
     }
 #pragma unroll
@@ -384,48 +386,44 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
     bool certain = true;
     if (a.n_group > 1) {
       // the group's best one or two, in every lane of the group
-      uint32_t b1 = s[0], b2 = VPL > 1 ? s[VPL > 1 ? 1 : 0] : 0u;
+      float b1 = s[0], b2 = VPL > 1 ? s[VPL > 1 ? 1 : 0] : neg_inf_f32();
       for (int off = 1; off < (1 << sp.lanes_log2); off <<= 1) {
-        const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, off), o2 = __shfl_xor_sync(0xFFFFFFFFu, b2, off);
-        b2 = max(min(b1, o1), max(b2, o2));
-        b1 = max(b1, o1);
+        const float o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, off), o2 = __shfl_xor_sync(0xFFFFFFFFu, b2, off);
+        b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+        b1 = fmaxf(b1, o1);
       }
-      uint32_t total = b1;  // group_top 1: the best key decides
+      float total = b1;  // group_top 1: the best key decides
       if (pair_sums) {
-        float v1 = value_of(b1), v2 = value_of(b2);
-        if (!biased) {
-          v1 = score(v1);
-          v2 = score(v2);
-        }
-        total = b1 == 0u ? 0u : key_of(b2 == 0u ? v1 : v1 + v2);
+        const float v1 = biased ? b1 : score(b1), v2 = biased ? b2 : score(b2);
+        total = b1 == neg_inf_f32() ? b1 : (b2 == neg_inf_f32() ? v1 : v1 + v2);
       }
+      // groups ahead of this one, a share of the comparisons in each of its lanes
+      const int lanes = 1 << sp.lanes_log2;
       int ahead = 0;
-#pragma unroll 4
-      for (int h = 0; h < a.n_group; ++h) {
-        const uint32_t o = __shfl_sync(0xFFFFFFFFu, total, h << sp.lanes_log2);
-        ahead += o > total || (o == total && h < g);
+      for (int h0 = 0; h0 < a.n_group; h0 += lanes) {
+        const int h = h0 + (lane & (lanes - 1));
+        const float o = __shfl_sync(0xFFFFFFFFu, total, h << sp.lanes_log2);
+        ahead += h < a.n_group && (o > total || (o == total && h < g));
       }
+      for (int off = 1; off < lanes; off <<= 1) ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, off);
       const bool in = g < a.n_group, keep = in && ahead < a.topk_group;
       if ((pair_sums || biased) && a.topk_group < a.n_group) {
-        const uint32_t worst = redux_min(keep ? total : 0xFFFFFFFFu), best = redux_max(in && !keep ? total : 0u);
-        const float w = value_of(worst), b = value_of(best);
-        certain = best == 0u || w - b > 2.0f * tol + 0x1p-20f * fmaxf(fabsf(w), fabsf(b));
+        const float w = redux_min(keep ? total : __int_as_float(0x7F800000));
+        const float b = redux_max(in && !keep ? total : neg_inf_f32());
+        certain = b == neg_inf_f32() || w - b > 2.0f * tol + 0x1p-20f * fmaxf(fabsf(w), fabsf(b));
       }
-      if (!keep) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) s[i] = 0u;
-      }
+      if (!keep) s[0] = neg_inf_f32();  // the lane never gives up a key
     }
 
     // the choice: lane j gets place j's key and the lane that had it; with a
     // bias also the first expert left out
     const int rounds = a.top_k + (biased && a.top_k < 32 ? 1 : 0);
-    uint32_t my_key = 0u;
+    float my_key = neg_inf_f32();
     int my_lane = 0;
     for (int j = 0; j < rounds; ++j) {
-      const uint32_t m = redux_max(s[0]);
+      const float m = redux_max(s[0]);
       const uint32_t have = __ballot_sync(0xFFFFFFFFu, s[0] == m);
-      if (m == 0u) break;
+      if (m == neg_inf_f32()) break;
       const int w = __ffs(have) - 1;
       if (lane == j) {
         my_key = m;
@@ -433,13 +431,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
       }
       const bool mine = lane == w;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) s[i] = mine ? (i + 1 < VPL ? s[i + 1 < VPL ? i + 1 : i] : 0u) : s[i];
+      for (int i = 0; i < VPL; ++i) s[i] = mine ? (i + 1 < VPL ? s[i + 1 < VPL ? i + 1 : i] : neg_inf_f32()) : s[i];
     }
+    const bool placed = my_key > neg_inf_f32();
     // equal keys of one lane come one after another, in expert order: how many went before this one
-    const uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, my_key, 1);
+    const float prev = __shfl_up_sync(0xFFFFFFFFu, my_key, 1);
     const int prev_lane = __shfl_up_sync(0xFFFFFFFFu, my_lane, 1);
     const uint32_t repeats =
-        __ballot_sync(0xFFFFFFFFu, lane > 0 && my_key != 0u && my_key == prev && my_lane == prev_lane);
+        __ballot_sync(0xFFFFFFFFu, lane > 0 && placed && my_key == prev && my_lane == prev_lane);
     int seen = 0;
     if (repeats != 0u) seen = lane - (31 - __clz(~repeats & (0xFFFFFFFFu >> (31 - lane))));
     int at = 0;
@@ -450,18 +449,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
       seen -= hit;
     }
     int id = -1;
-    if (my_key != 0u)
+    if (placed)
       id = (my_lane >> sp.lanes_log2) * sp.size + (my_lane & ((1 << sp.lanes_log2) - 1)) * sp.per_lane + at;
     float lid = id >= 0 ? load_logit<kBf16>(row, id) : 0.0f;
     if (biased) {
-      uint32_t next = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
-      const uint32_t rest = a.top_k == 32 ? redux_max(s[0]) : 0u;  // of 32 places, the first expert left out
+      float next = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
+      const float rest = a.top_k == 32 ? redux_max(s[0]) : neg_inf_f32();  // of 32 places, the first expert left out
       if (lane == 31) next = rest;
       bool sure = true;
-      if (lane < a.top_k && next != 0u) {
-        const float v = value_of(my_key), n = value_of(next);
-        sure = v - n > tol + 0x1p-22f * fmaxf(fabsf(v), fabsf(n));
-      }
+      if (lane < a.top_k && next > neg_inf_f32())
+        sure = my_key - next > tol + 0x1p-22f * fmaxf(fabsf(my_key), fabsf(next));
       if (!__all_sync(0xFFFFFFFFu, sure)) {
         // keys in one another's reach: certain only between equal logits with equal biases
         const float bid = id >= 0 ? __ldg(a.bias + id) : 0.0f;
@@ -596,7 +593,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_bwd_kernel(RouteBw
     float m = neg_inf_f32();
 #pragma unroll
     for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
-    m = value_of(redux_max(key_of(m)));  // of logits without NaN
+    m = redux_max(m);
     float sum = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
