@@ -932,6 +932,10 @@ static int run_layout(LayoutArgs a, cudaStream_t stream) {
   // one cluster: a CTA per 1024 entries, up to eight
   unsigned ctas = 1;
   while (ctas < kLayoutMaxCtas && static_cast<int64_t>(ctas) * kLayoutThreads < a.n) ctas *= 2;
+  if (ctas == 1) {
+    moe_layout_kernel<<<1, kLayoutThreads, layout_smem(a.E), stream>>>(a);
+    return launched();
+  }
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim.x = ctas;
