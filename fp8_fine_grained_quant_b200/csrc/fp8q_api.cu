@@ -786,10 +786,11 @@ int fp8_gemm_wgrad(const uint8_t* q_dy_t, const float* s_dy, const uint8_t* q_x_
 template <int VPL, bool kBf16>
 static void launch_route_vpl(const RouteArgs& a, const RouteSplit& sp, unsigned grid, size_t smem,
                              cudaStream_t stream) {
-  if (a.sigmoid)
-    moe_route_kernel<VPL, kBf16, true><<<grid, 32 * kRouteWarps, smem, stream>>>(a, sp);
-  else
-    moe_route_kernel<VPL, kBf16, false><<<grid, 32 * kRouteWarps, smem, stream>>>(a, sp);
+  const auto kernel = a.sigmoid ? (a.bias ? moe_route_kernel<VPL, kBf16, true, true>
+                                          : moe_route_kernel<VPL, kBf16, true, false>)
+                                : (a.bias ? moe_route_kernel<VPL, kBf16, false, true>
+                                          : moe_route_kernel<VPL, kBf16, false, false>);
+  kernel<<<grid, 32 * kRouteWarps, smem, stream>>>(a, sp);
 }
 
 template <bool kBf16>

@@ -109,84 +109,119 @@ __device__ __forceinline__ float route_weight(float l, bool found, bool sigmoid,
   return found ? scale * p : 0.0f;
 }
 
-// The choice in binary64.  keys: the warp's E doubles of shared memory.
+// Scores in binary64.  Out of line: few rows need them, and one copy of the
+// exponential keeps their code short (a cold path's time is its instruction
+// fetches as much as its arithmetic).
+__device__ __noinline__ double exp_f64(double x) { return exp(x); }
+__device__ __noinline__ double score_f64(bool sigmoid, float l, float row_max, double sum) {
+  const double x = exp_f64(sigmoid ? -static_cast<double>(l) : static_cast<double>(l) - static_cast<double>(row_max));
+  return sigmoid ? 1.0 / (1.0 + x) : x / sum;
+}
+
+// The sum of exp(l - row_max) over a row in binary64.
+template <bool kBf16>
+__device__ __noinline__ double row_sum_f64(const void* row, int E, float row_max) {
+  double sum = 0.0;
+  for (int e = threadIdx.x & 31; e < E; e += 32) {
+    const float l = load_logit<kBf16>(row, e);
+    if (l > neg_inf_f32()) sum += exp_f64(static_cast<double>(l) - static_cast<double>(row_max));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+  return sum;
+}
+
+// The whole choice in binary64.  keys: the warp's E doubles of shared memory.
 // Returns the id of place `lane` (or -1).
 template <bool kBf16>
 __device__ __noinline__ int route_choose_f64(const RouteArgs& a, const void* row, double* keys, float row_max) {
+  constexpr int kAhead = 4;
   const int lane = threadIdx.x & 31;
   const int E = a.E;
-  double sum = 0.0;
-  if (!a.sigmoid) {
-    for (int e = lane; e < E; e += 32) {
-      const float l = load_logit<kBf16>(row, e);
-      if (l > neg_inf_f32()) sum += exp(static_cast<double>(l) - static_cast<double>(row_max));
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-  }
+  const double sum = a.sigmoid ? 0.0 : row_sum_f64<kBf16>(row, E, row_max);
   const bool by_score = a.bias != nullptr || (a.n_group > 1 && a.group_top == 2);
   for (int e = lane; e < E; e += 32) {
     const float l = load_logit<kBf16>(row, e);
     double k = static_cast<double>(l);
-    if (l > neg_inf_f32() && by_score) {
-      k = a.sigmoid ? 1.0 / (1.0 + exp(-k)) : exp(k - static_cast<double>(row_max)) / sum;
-      if (a.bias != nullptr) {
-        k += static_cast<double>(a.bias[e]);
-        if (!(k > neg_inf_f64())) k = neg_inf_f64();
-      }
+    if (by_score) {
+      double p = score_f64(a.sigmoid, l, row_max, sum);
+      if (a.bias != nullptr) p += static_cast<double>(__ldg(a.bias + e));
+      k = l > neg_inf_f32() && p > neg_inf_f64() ? p : neg_inf_f64();
     }
-    keys[e] = k;
+    keys[e] = k + 0.0;  // -0 as +0
   }
   __syncwarp();
   if (a.n_group > 1) {
     const int size = E / a.n_group;
-    double total = neg_inf_f64();
-    if (lane < a.n_group) {
-      double b1 = neg_inf_f64(), b2 = neg_inf_f64();
-      for (int i = 0; i < size; ++i) {
-        const double k = keys[lane * size + i];
+    int lanes = 32;  // of a group
+    while (lanes * a.n_group > 32) lanes >>= 1;
+    const int g = lane / lanes;
+    double b1 = neg_inf_f64(), b2 = neg_inf_f64();
+    if (g < a.n_group) {
+#pragma unroll 4
+      for (int i = lane & (lanes - 1); i < size; i += lanes) {
+        const double k = keys[g * size + i];
         b2 = fmax(b2, fmin(b1, k));
         b1 = fmax(b1, k);
       }
-      total = a.group_top == 2 && b2 > neg_inf_f64() ? b1 + b2 : b1;
     }
+    for (int off = 1; off < lanes; off <<= 1) {
+      const double o1 = __shfl_xor_sync(0xFFFFFFFFu, b1, off), o2 = __shfl_xor_sync(0xFFFFFFFFu, b2, off);
+      b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+      b1 = fmax(b1, o1);
+    }
+    const double total = a.group_top == 2 && b2 > neg_inf_f64() ? b1 + b2 : b1;
     int ahead = 0;
     for (int h = 0; h < a.n_group; ++h) {
-      const double o = __shfl_sync(0xFFFFFFFFu, total, h);
-      ahead += o > total || (o == total && h < lane);
+      const double o = __shfl_sync(0xFFFFFFFFu, total, h * lanes);
+      ahead += o > total || (o == total && h < g);
     }
-    const uint32_t keep = __ballot_sync(0xFFFFFFFFu, lane < a.n_group && ahead < a.topk_group);
+    const uint32_t keep = __ballot_sync(0xFFFFFFFFu, g < a.n_group && ahead < a.topk_group);
     __syncwarp();
     for (int e = lane; e < E; e += 32) {
-      if (!((keep >> (e / size)) & 1u))
+      if (!((keep >> (e / size * lanes)) & 1u))
         keys[e] = neg_inf_f64();
       else if (by_score && a.bias == nullptr)
-        keys[e] = static_cast<double>(load_logit<kBf16>(row, e));
+        keys[e] = static_cast<double>(load_logit<kBf16>(row, e)) + 0.0;
     }
     __syncwarp();
   }
+  // the lane's best key and its expert (the first of equals)
+  double best = neg_inf_f64();
+  int at = E;
+  auto rescan = [&] {
+    best = neg_inf_f64();
+    at = E;
+    for (int e0 = lane; e0 < E; e0 += 32 * kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int e = e0 + 32 * i;
+        const double k = e < E ? keys[e] : neg_inf_f64();
+        if (k > best) {
+          best = k;
+          at = e;
+        }
+      }
+    }
+  };
+  rescan();
   int mine = -1;
   for (int j = 0; j < a.top_k; ++j) {
-    double best = neg_inf_f64();
-    int at = E;
-    for (int e = lane; e < E; e += 32) {
-      if (keys[e] > best) {
-        best = keys[e];
-        at = e;
-      }
+    // order-preserving integers of the keys, the larger half first, then the lower expert
+    const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(best));
+    const unsigned long long o = bits ^ (bits >> 63 ? ~0ull : 0x8000000000000000ull);
+    const uint32_t hi = static_cast<uint32_t>(o >> 32), lo = static_cast<uint32_t>(o);
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, at < E ? hi : 0u);
+    if (top == 0u) break;  // no lane has a key
+    bool in = at < E && hi == top;
+    const uint32_t low = __reduce_max_sync(0xFFFFFFFFu, in ? lo : 0u);
+    in = in && lo == low;
+    const int w = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, in ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
+    if (lane == j) mine = w;
+    if (lane == (w & 31)) {  // the lane that scans w
+      keys[w] = neg_inf_f64();
+      rescan();
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const double o = __shfl_xor_sync(0xFFFFFFFFu, best, off);
-      const int oa = __shfl_xor_sync(0xFFFFFFFFu, at, off);
-      if (o > best || (o == best && oa < at)) {
-        best = o;
-        at = oa;
-      }
-    }
-    if (!(best > neg_inf_f64())) break;  // uniform: every lane holds the same best
-    if (lane == j) mine = at;
-    if (lane == (at & 31)) keys[at] = neg_inf_f64();  // the lane that scans `at`
     __syncwarp();
   }
   return mine;
@@ -294,6 +329,7 @@ __device__ __forceinline__ void share_values(const uint32_t (&w)[VPL], bool vect
   }
 }
 
+constexpr int kExactVpl = 8;  // up to this share, a comparison that FP32 leaves open is settled in registers
 constexpr int kRouteWarps = 4;
 constexpr int kRouteCtasPerSm = 8;  // up to eight experts a lane: 64 registers
 
@@ -306,9 +342,12 @@ constexpr int kRouteCtasPerSm = 8;  // up to eight experts a lane: 64 registers
 // Without a bias experts are compared by their logits, exactly.  With one, and
 // for group sums, FP32 keys are compared, and each comparison that decides
 // (neighbours in the choice, the first expert left out, the worst group kept
-// against the best one dropped) must be wider than the keys' error; a row
-// where one is not goes to route_choose_f64.  Equal keys of equal logits and
-// biases need no proof.  The errors, by exp_approx's:
+// against the best one dropped) must be wider than the keys' error.  Equal keys
+// of equal logits and biases need no proof.  Where one is not (about one row in
+// a thousand), the keys within reach of the comparison are evaluated in
+// binary64, a key a lane: the best of every group, or the chosen and those next
+// to the last of them.  Shares above eight experts, and more than 32 keys in
+// reach, take route_choose_f64.  The errors, by exp_approx's:
 //   sigmoid  p (1 - p) (2 + |x|) 2^-23 <= 2^-23, + 2^-24 from 1 + e and 2^-23
 //            from rcp: below 2^-21.6 a key; + 2^-24 |key| from adding the bias;
 //   softmax  at most 30 * 2^-23 of p from the row's sum (37 additions, and
@@ -316,7 +355,7 @@ constexpr int kRouteCtasPerSm = 8;  // up to eight experts a lane: 64 registers
 //            keys, as their p sum to at most 1;
 // so two keys further apart than 2^-20 (sigmoid) or 2^-17 (softmax) + 2^-22 of
 // the larger are in order; for sums of two keys, twice that.
-template <int VPL, bool kBf16, bool kSigmoid>
+template <int VPL, bool kBf16, bool kSigmoid, bool biased>
 __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm : 1) moe_route_kernel(RouteArgs a, RouteSplit sp) {
   extern __shared__ double route_keys[];  // [kRouteWarps][E]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -324,15 +363,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
   const int first = (lane & ((1 << sp.lanes_log2) - 1)) * sp.per_lane;
   const int base = g * sp.size + first;
   const int count = g < a.n_group ? max(0, min(sp.per_lane, sp.size - first)) : 0;
-  const bool biased = a.bias != nullptr;
   const bool pair_sums = a.n_group > 1 && a.group_top == 2;
   const bool stats = !kSigmoid && (biased || pair_sums || !a.renorm);  // something needs the row's softmax
   constexpr float tol = kSigmoid ? 0x1p-20f : 0x1p-17f;
-  float bias[VPL];  // -inf: never chosen
+  float bias[biased ? VPL : 1];  // -inf: never chosen
+  if constexpr (biased) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    bias[i] = biased && i < count ? __ldg(a.bias + base + i) : 0.0f;
-    if (!(bias[i] > neg_inf_f32())) bias[i] = neg_inf_f32();
+    for (int i = 0; i < VPL; ++i) {
+      bias[i] = i < count ? __ldg(a.bias + base + i) : 0.0f;
+      if (!(bias[i] > neg_inf_f32())) bias[i] = neg_inf_f32();
+    }
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
@@ -364,7 +404,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
 
     // keys: the logits (-0 as +0), or score + bias; -inf: never chosen
     float key[VPL], s[VPL];
-    if (!biased) {
+    if constexpr (!biased) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = l[i] + 0.0f;
     } else {
@@ -406,25 +446,62 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
         ahead += h < a.n_group && (o > total || (o == total && h < g));
       }
       for (int off = 1; off < lanes; off <<= 1) ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, off);
-      const bool in = g < a.n_group, keep = in && ahead < a.topk_group;
+      const bool in = g < a.n_group;
+      bool keep = in && ahead < a.topk_group;
       if ((pair_sums || biased) && a.topk_group < a.n_group) {
         const float w = redux_min(keep ? total : __int_as_float(0x7F800000));
         const float b = redux_max(in && !keep ? total : neg_inf_f32());
-        certain = b == neg_inf_f32() || w - b > 2.0f * tol + 0x1p-20f * fmaxf(fabsf(w), fabsf(b));
+        if (!(b == neg_inf_f32() || w - b > 2.0f * tol + 0x1p-20f * fmaxf(fabsf(w), fabsf(b)))) {
+          if constexpr (VPL <= kExactVpl) {
+            // the groups' sums in binary64, of the keys that can be among their best: each lane's
+            // next largest in turn while some lane has one
+            const double sum = kSigmoid ? 0.0 : row_sum_f64<kBf16>(row, a.E, row_max);
+            const float last = a.group_top == 2 ? b2 : b1;
+            const float from = biased ? last - 2.0f * (tol + 0x1p-22f * fabsf(last)) : last;
+            double d1 = neg_inf_f64(), d2 = neg_inf_f64();
+            uint32_t used = 0u;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+              const bool can = s[j] > neg_inf_f32() && s[j] >= from;
+              if (!__any_sync(0xFFFFFFFFu, can)) break;
+              int at = -1;  // the lane's first unused key s[j]
+#pragma unroll
+              for (int i = 0; i < VPL; ++i)
+                if (at < 0 && key[i] == s[j] && !((used >> i) & 1u)) at = i;
+              if (can) {
+                used |= 1u << at;
+                double v = score_f64(kSigmoid, load_logit<kBf16>(row, base + at), row_max, sum);
+                if constexpr (biased) v += static_cast<double>(__ldg(a.bias + base + at));
+                d2 = fmax(d2, fmin(d1, v));
+                d1 = fmax(d1, v);
+              }
+            }
+            for (int off = 1; off < lanes; off <<= 1) {
+              const double o1 = __shfl_xor_sync(0xFFFFFFFFu, d1, off), o2 = __shfl_xor_sync(0xFFFFFFFFu, d2, off);
+              d2 = fmax(fmin(d1, o1), fmax(d2, o2));
+              d1 = fmax(d1, o1);
+            }
+            const double sum2 = a.group_top == 2 && d2 > neg_inf_f64() ? d1 + d2 : d1;
+            ahead = 0;
+            for (int h = 0; h < a.n_group; ++h) {
+              const double o = __shfl_sync(0xFFFFFFFFu, sum2, h << sp.lanes_log2);
+              ahead += o > sum2 || (o == sum2 && h < g);
+            }
+            keep = in && ahead < a.topk_group;
+          } else {
+            certain = false;
+          }
+        }
       }
       if (!keep) s[0] = neg_inf_f32();  // the lane never gives up a key
     }
 
     // the choice: lane j gets place j's key and the lane that had it; with a
     // bias also the first expert left out
-    const int rounds = a.top_k + (biased && a.top_k < 32 ? 1 : 0);
     float my_key = neg_inf_f32();
     int my_lane = 0;
-    for (int j = 0; j < rounds; ++j) {
-      const float m = redux_max(s[0]);
-      const uint32_t have = __ballot_sync(0xFFFFFFFFu, s[0] == m);
-      if (m == neg_inf_f32()) break;
-      const int w = __ffs(have) - 1;
+    auto place = [&](int j, float m) {
+      const int w = __ffs(__ballot_sync(0xFFFFFFFFu, s[0] == m)) - 1;
       if (lane == j) {
         my_key = m;
         my_lane = w;
@@ -432,38 +509,80 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
       const bool mine = lane == w;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) s[i] = mine ? (i + 1 < VPL ? s[i + 1 < VPL ? i + 1 : i] : neg_inf_f32()) : s[i];
-    }
-    const bool placed = my_key > neg_inf_f32();
-    // equal keys of one lane come one after another, in expert order: how many went before this one
-    const float prev = __shfl_up_sync(0xFFFFFFFFu, my_key, 1);
-    const int prev_lane = __shfl_up_sync(0xFFFFFFFFu, my_lane, 1);
-    const uint32_t repeats =
-        __ballot_sync(0xFFFFFFFFu, lane > 0 && placed && my_key == prev && my_lane == prev_lane);
-    int seen = 0;
-    if (repeats != 0u) seen = lane - (31 - __clz(~repeats & (0xFFFFFFFFu >> (31 - lane))));
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const bool hit = __shfl_sync(0xFFFFFFFFu, key[i], my_lane) == my_key;
-      if (hit && seen == 0) at = i;
-      seen -= hit;
+    };
+    const int rounds = a.top_k + (biased && a.top_k < 32 ? 1 : 0);
+    for (int j = 0; j < rounds; ++j) {
+      const float m = redux_max(s[0]);
+      if (m == neg_inf_f32()) break;
+      place(j, m);
     }
     int id = -1;
-    if (placed)
-      id = (my_lane >> sp.lanes_log2) * sp.size + (my_lane & ((1 << sp.lanes_log2) - 1)) * sp.per_lane + at;
-    float lid = id >= 0 ? load_logit<kBf16>(row, id) : 0.0f;
-    if (biased) {
+    float lid = 0.0f;  // its logit
+    auto find = [&] {
+      const bool placed = my_key > neg_inf_f32();
+      // equal keys of one lane come one after another, in expert order: how many went before this one
+      const float prev = __shfl_up_sync(0xFFFFFFFFu, my_key, 1);
+      const int prev_lane = __shfl_up_sync(0xFFFFFFFFu, my_lane, 1);
+      const uint32_t repeats =
+          __ballot_sync(0xFFFFFFFFu, lane > 0 && placed && my_key == prev && my_lane == prev_lane);
+      int seen = 0;
+      if (repeats != 0u) seen = lane - (31 - __clz(~repeats & (0xFFFFFFFFu >> (31 - lane))));
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const bool hit = __shfl_sync(0xFFFFFFFFu, key[i], my_lane) == my_key;
+        if (hit && seen == 0) at = i;
+        seen -= hit;
+      }
+      if (placed) {
+        id = (my_lane >> sp.lanes_log2) * sp.size + (my_lane & ((1 << sp.lanes_log2) - 1)) * sp.per_lane + at;
+        lid = load_logit<kBf16>(row, id);
+      }
+    };
+    find();
+    if constexpr (biased) {
       float next = __shfl_down_sync(0xFFFFFFFFu, my_key, 1);
       const float rest = a.top_k == 32 ? redux_max(s[0]) : neg_inf_f32();  // of 32 places, the first expert left out
       if (lane == 31) next = rest;
       bool sure = true;
       if (lane < a.top_k && next > neg_inf_f32())
         sure = my_key - next > tol + 0x1p-22f * fmaxf(fabsf(my_key), fabsf(next));
-      if (!__all_sync(0xFFFFFFFFu, sure)) {
+      if (certain && !__all_sync(0xFFFFFFFFu, sure)) {
         // keys in one another's reach: certain only between equal logits with equal biases
-        const float bid = id >= 0 ? __ldg(a.bias + id) : 0.0f;
+        float bid = id >= 0 ? __ldg(a.bias + id) : 0.0f;
         const float nl = __shfl_down_sync(0xFFFFFFFFu, lid, 1), nb = __shfl_down_sync(0xFFFFFFFFu, bid, 1);
-        certain = certain && __all_sync(0xFFFFFFFFu, sure || (lane < 31 && lid == nl && bid == nb));
+        certain = __all_sync(0xFFFFFFFFu, sure || (lane < 31 && lid == nl && bid == nb));
+        if (VPL <= kExactVpl && !certain && a.top_k < 32) {
+          // more places, until the next key cannot reach the last that counts
+          const float kth = __shfl_sync(0xFFFFFFFFu, my_key, a.top_k - 1);
+          const float reach = kth - 2.0f * (tol + 0x1p-22f * fabsf(kth));
+          float m = redux_max(s[0]);
+          for (int j = rounds; j < 32 && m > neg_inf_f32() && m >= reach; ++j) {
+            place(j, m);
+            m = redux_max(s[0]);
+          }
+          if (!(m > neg_inf_f32() && m >= reach)) {  // all within reach have a lane
+            find();
+            bid = id >= 0 ? __ldg(a.bias + id) : 0.0f;
+            // their keys in binary64, one a lane, and their order
+            const double sum = kSigmoid ? 0.0 : row_sum_f64<kBf16>(row, a.E, row_max);
+            const double v = id >= 0 ? score_f64(kSigmoid, lid, row_max, sum) + static_cast<double>(bid) : neg_inf_f64();
+            const int n = __popc(__ballot_sync(0xFFFFFFFFu, id >= 0));
+            int ahead = 0, mine = -1;
+            for (int j = 0; j < n; ++j) {
+              const double o = __shfl_sync(0xFFFFFFFFu, v, j);
+              const int oi = __shfl_sync(0xFFFFFFFFu, id, j);
+              ahead += o > v || (o == v && oi < id);
+            }
+            for (int j = 0; j < n; ++j) {
+              const int oa = __shfl_sync(0xFFFFFFFFu, ahead, j), oi = __shfl_sync(0xFFFFFFFFu, id, j);
+              if (oa == lane) mine = oi;
+            }
+            id = mine;
+            lid = id >= 0 ? load_logit<kBf16>(row, id) : 0.0f;
+            certain = true;
+          }
+        }
       }
     }
     if (!certain) {

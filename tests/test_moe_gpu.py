@@ -143,6 +143,57 @@ def test_route_keys_closer_than_fp32(dev, score, G, KG):
                      topk_group=KG, group_top=2)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,KG,GT", [(256, 1, 1, 1), (256, 8, 4, 2), (64, 8, 3, 2), (64, 4, 2, 1), (60, 5, 2, 2),
+                                       (384, 8, 4, 2), (8, 1, 1, 1)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_settles_single_close_comparisons(dev, score, E, G, KG, GT, biased):
+    """A few keys of a row an ulp apart, next to the choice's border or inside it,
+    and pairs of groups whose best keys differ by an ulp: the comparisons that FP32
+    leaves open are settled by the exact keys, the others kept."""
+    rng = np.random.default_rng(E + G + KG)
+    T, k, size = 400, min(6, E // 2), E // G
+    l = (1.5 * rng.standard_normal((T, E))).astype(np.float32)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32) if biased else None
+    if biased and G > 1:
+        bias[size:2 * size] = bias[:size]                 # groups 0 and 1 can be twins
+    elif biased:
+        bias[E // 2:] = bias[:E // 2]
+    step = np.where(rng.random((T, E)) < 0.5, np.float32(np.inf), np.float32(-np.inf))
+    for t in range(T):
+        if G > 1 and t % 2:
+            l[t, size:2 * size] = l[t, :size]
+            e = rng.integers(0, size)
+            l[t, size + e] = np.nextafter(l[t, e], step[t, e])
+        else:
+            for e in rng.choice(E // 2, min(4, E // 2), replace=False):   # e and e + E/2, an ulp apart or equal
+                l[t, e + E // 2] = np.nextafter(l[t, e], step[t, e]) if rng.random() < 0.8 else l[t, e]
+            order = np.argsort(-l[t, :E // 2])
+            e = order[min(k // 2, E // 2 - 1)]
+            l[t, e + E // 2] = np.nextafter(l[t, e], step[t, e])
+    for renorm in (True, False):
+        _check_route(dev, torch.from_numpy(l).to(dev), l.astype(np.float64), k, score=score, bias=bias, n_group=G,
+                     topk_group=KG, group_top=GT, renorm=renorm)
+
+
+def test_route_settles_keys_of_different_experts_with_different_biases(dev):
+    """p_i + b_i and p_j + b_j equal to FP32's last digits for unequal logits and
+    biases, at the border of the choice."""
+    rng = np.random.default_rng(31)
+    T, E, k = 600, 128, 8
+    l = (1.5 * rng.standard_normal((T, E))).astype(np.float32)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    for t in range(T):
+        key = 1 / (1 + np.exp(-l[t].astype(np.float64))) + bias
+        order = np.argsort(-key)
+        for place in (k - 1, 2):                           # the last that counts, and one inside
+            i, j = order[place], order[rng.integers(40, E)]
+            p = key[i] - bias[j]
+            if 0.01 < p < 0.99:
+                l[t, j] = np.float32(np.log(p / (1 - p)))
+    _check_route(dev, torch.from_numpy(l).to(dev), l.astype(np.float64), k, score="sigmoid", bias=bias)
+
+
 @pytest.mark.parametrize("l0", [-120.0, -80.0, 60.0])
 def test_route_sigmoid_ratios_survive_underflow(dev, l0):
     rng = np.random.default_rng(13)
@@ -407,6 +458,23 @@ def test_streams_and_graph_replay(dev):
         ref, mag = moe.combine(moe.bf16_to_f32(yb).astype(np.float64), osl, ow)
         err = np.abs(moe.bf16_to_f32(bf16_bits_of(hold["out"])).astype(np.float64) - ref)
         assert np.all(err <= 100 * U * mag + 2.0 ** -8 * (np.abs(ref) + mag * 100 * U) + TINY)
+
+
+def test_misaligned_tensors_are_refused(dev):
+    """A contiguous view that starts off the alignment raises the library's error,
+    and the next call works."""
+    x = torch.zeros(4 * 256 + 8, dtype=torch.bfloat16, device=dev)[8:].view(4, 256)      # 16 bytes in: 32 needed
+    slots = torch.zeros((4, 2), dtype=torch.int32, device=dev)
+    with pytest.raises(fq.Fp8qError) as e:
+        fq.fp8_moe_dispatch_1x128(x, slots, 128)
+    assert e.value.status == fq.ERR_ALIGN
+    with pytest.raises(fq.Fp8qError):
+        fq.fp8_moe_combine(torch.zeros(128 * 128 + 4, dtype=torch.bfloat16, device=dev)[4:].view(128, 128), slots)
+    assert torch.all(fq.fp8_moe_combine(torch.zeros((128, 128), dtype=torch.bfloat16, device=dev), slots) == 0)
+    with pytest.raises(ValueError, match="dy may not be y"):
+        y = torch.zeros((128, 128), dtype=torch.bfloat16, device=dev)
+        fq.fp8_moe_combine_bwd(torch.zeros((4, 128), dtype=torch.bfloat16, device=dev), y, slots,
+                               torch.zeros((4, 2), device=dev), dy=y)
 
 
 def test_results_do_not_depend_on_the_run(dev):
