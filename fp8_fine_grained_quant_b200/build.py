@@ -63,7 +63,8 @@ def build_calls(force: bool = False) -> Path:
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
     cmd += ["-I%s" % i for i in includes] + ["-o", str(tmp), str(CALLS_SOURCE), "-L" + str(PKG), "-l:" + LIB.name,
                                            "-Wl,-rpath,$ORIGIN"]
-    cmd += ["-L%s" % (base / "lib"), "-L%s" % (cuda / "lib64"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
+    cmd += ["-L%s" % (base / "lib"), "-L%s" % (cuda / "lib64")]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
     subprocess.run(cmd, check=True)
     os.replace(tmp, CALLS)
     return CALLS

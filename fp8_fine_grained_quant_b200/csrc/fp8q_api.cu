@@ -818,9 +818,9 @@ static void launch_route(const RouteArgs& a, int num_sms, cudaStream_t stream) {
   }
 }
 
-// The instance with the fewest experts a lane: exact up to 256 experts (a row of
-// 160 in the 8-a-lane instance costs a third more than in its own), in steps
-// above.
+// The instance with the fewest experts a lane: exact up to 256 experts, in steps
+// above.  (16384 rows of 160, every logit's gradient: 10.0 us at eight a lane,
+// 8.4 at five.)
 template <int VPL, bool kBf16>
 static void launch_route_bwd(const RouteBwdArgs& a, cudaStream_t stream) {
   if constexpr (VPL < 32) {
@@ -933,10 +933,6 @@ static int run_layout(LayoutArgs a, cudaStream_t stream) {
   // one cluster: a CTA per 1024 entries, up to eight
   unsigned ctas = 1;
   while (ctas < kLayoutMaxCtas && static_cast<int64_t>(ctas) * kLayoutThreads < a.n) ctas *= 2;
-  if (ctas == 1) {
-    moe_layout_kernel<<<1, kLayoutThreads, layout_smem(a.E), stream>>>(a);
-    return launched();
-  }
   cudaLaunchAttribute cluster;
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim.x = ctas;

@@ -61,7 +61,8 @@ void spec(const Tensor& t, const char* name, Types types, int64_t lo = 0, int64_
   bool ok = false;
   for (at::ScalarType s : types) ok = ok || t.scalar_type() == s;
   if (!ok) bad_type(name, ": dtype ", t.scalar_type(), " is not supported here");
-  if (t.dim() < lo || t.dim() > hi) bad_value(name, ": expected ", lo, lo == hi ? "" : text(" to ", hi), " dims, got ", t.dim());
+  if (t.dim() < lo || t.dim() > hi)
+    bad_value(name, ": expected ", lo, lo == hi ? "" : text(" to ", hi), " dims, got ", t.dim());
   if (!t.is_contiguous()) bad_value(name, " must be contiguous");
 }
 void holds(const Tensor& t, const char* name, int64_t n) {
@@ -388,7 +389,8 @@ py::tuple swiglu_bwd(const Tensor& dh, const Tensor& qc, const Tensor& sc, const
   const int64_t rows = dh.size(0), inter = dh.size(1), nt = inter / kTile;
   multiple(inter, "inter");
   if (qc.size(0) != rows || qc.size(1) != 2 * inter)
-    bad_value("qc is [", qc.size(0), ", ", qc.size(1), "], dh [", rows, ", ", inter, "] needs [", rows, ", ", 2 * inter, "]");
+    bad_value("qc is [", qc.size(0), ", ", qc.size(1), "], dh [", rows, ", ", inter, "] needs [", rows, ", ",
+              2 * inter, "]");
   holds(sc, "sc", rows * 2 * nt);
   buffer(dc, "dc", kBf16, rows * 2 * inter);
   buffer(q, "q", kFp8, rows * 2 * inter);
@@ -413,8 +415,8 @@ py::tuple swiglu_bwd(const Tensor& dh, const Tensor& qc, const Tensor& sc, const
   return py::make_tuple(a, py::make_tuple(b, c));
 }
 
-py::tuple ckpt_128x1_t(const Tensor& q, const Tensor& s, std::optional<int64_t> padded, const Opt& qt, const Opt& st,
-                       const py::object& stream) {
+py::tuple ckpt_128x1_t(const Tensor& q, const Tensor& s, std::optional<int64_t> padded, const Opt& qt,
+                       const Opt& st, const py::object& stream) {
   spec(q, "q", kFp8, 2, 2);
   spec(s, "s", kF32);
   const int64_t M = q.size(0), K = q.size(1);

@@ -74,7 +74,8 @@ def test_route(dev, T, E, k, dtype, score):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("E,G,KG,GT,k", [(256, 8, 4, 2, 8), (160, 8, 3, 1, 6), (64, 8, 1, 2, 8), (64, 32, 5, 2, 6),
                                          (60, 5, 2, 2, 7), (60, 3, 2, 1, 8), (32, 32, 4, 1, 4), (512, 16, 16, 2, 8),
-                                         (96, 2, 1, 2, 8), (1024, 4, 2, 2, 8), (8, 4, 2, 2, 4), (320, 10, 3, 2, 10)])
+                                         (96, 2, 1, 2, 8), (1024, 4, 2, 2, 8), (8, 4, 2, 2, 4), (320, 10, 3, 2, 10),
+                                         (1020, 17, 5, 2, 8), (990, 30, 10, 1, 8)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True])
 def test_route_groups(dev, E, G, KG, GT, k, dtype, score, biased):
