@@ -36,7 +36,8 @@
  *    the stacked row counts E*N, G*N and E*cap; a GEMM's count of 128-row
  *    output tiles times its column tiles (times E for the masked layout) stays
  *    below 2^31 - 2^16; larger shapes return FP8Q_ERR_SHAPE.
- *  - Non-finite inputs are outside the contract (results unspecified, no fault).
+ *  - Non-finite inputs are outside the contract (results unspecified, no fault),
+ *    except where an entry point gives them a meaning (the router's masks).
  *  - Every on-device wait is bounded (default 4 s, see fp8q_set_wait_timeout_ns);
  *    a wait that runs out records FP8Q_ERR_TIMEOUT in a device status word
  *    (one per device), the kernel lets its copies and MMAs in flight finish

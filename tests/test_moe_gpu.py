@@ -19,7 +19,7 @@ import torch
 import oracle
 import fp8_fine_grained_quant_b200 as fq
 from oracle import moe
-from parity import bf16_bits_of, bytes_of, to_torch_bf16
+from parity import assert_gemm_close, bf16_bits_of, bytes_of, to_torch_bf16
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -459,6 +459,88 @@ def test_streams_and_graph_replay(dev):
         ref, mag = moe.combine(moe.bf16_to_f32(yb).astype(np.float64), osl, ow)
         err = np.abs(moe.bf16_to_f32(bf16_bits_of(hold["out"])).astype(np.float64) - ref)
         assert np.all(err <= 100 * U * mag + 2.0 ** -8 * (np.abs(ref) + mag * 100 * U) + TINY)
+
+
+def test_masked_layer(dev):
+    """A serving layer from logits to output: route -> masked layout -> dispatch ->
+    GEMM1 -> SwiGLU -> GEMM2 -> combine, captured in a graph and replayed, each step
+    against the oracle on its own inputs.  One expert runs out of capacity."""
+    rng = np.random.default_rng(41)
+    T, E, k, D, I, cap = 200, 6, 2, 256, 128, 128
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l[:, 2] += 2.0                                                  # over 128 tokens choose expert 2
+    x = _bf16(rng, (T, D))
+    logits, xt = torch.from_numpy(l).to(dev), to_torch_bf16(x, dev)
+    qw1, sw1 = fq.fp8_quant_w_128x128(to_torch_bf16(_bf16(rng, (E, 2 * I, D), 0.06), dev))
+    qw2, sw2 = fq.fp8_quant_w_128x128(to_torch_bf16(_bf16(rng, (E, D, I), 0.09), dev))
+    q = torch.zeros((E, cap, D), dtype=torch.uint8, device=dev)
+    s = torch.ones((E, cap, D // 128), device=dev)
+    c1 = torch.zeros((E, cap, 2 * I), dtype=torch.bfloat16, device=dev)
+    y = torch.zeros((E, cap, D), dtype=torch.bfloat16, device=dev)
+    r = {}
+
+    def layer():
+        r["ids"], r["w"] = fq.fp8_moe_route(logits, k)
+        r["slots"], r["m"] = fq.fp8_moe_layout_masked(r["ids"], E, cap)
+        fq.fp8_moe_dispatch_1x128(xt, r["slots"], E * cap, q=q, s=s)
+        fq.fp8_grouped_gemm_masked(q, s, qw1, sw1, r["m"], out=c1)
+        r["qh"], r["sh"] = fq.fp8_swiglu_quant_1x128(c1, masked_m=r["m"])
+        fq.fp8_grouped_gemm_masked(r["qh"], r["sh"], qw2, sw2, r["m"], out=y)
+        r["out"] = fq.fp8_moe_combine(y, r["slots"], r["w"])
+
+    layer()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer()
+    graph.replay()
+    torch.cuda.synchronize(dev)
+    assert fq.get_device_error(device=dev) == fq.OK
+    oi, ow = moe.route(l, k)
+    osl, om = moe.layout_masked(oi, E, cap)
+    assert om[2] == cap and (osl < 0).any()
+    assert np.array_equal(r["slots"].cpu().numpy(), osl) and np.array_equal(r["m"].cpu().numpy(), om)
+    oq, _ = oracle.quant_act_1x128(x)
+    tok, j = np.nonzero(osl >= 0)
+    assert np.array_equal(q.cpu().numpy().reshape(E * cap, D)[osl[tok, j]], oq[tok])
+    ref1 = oracle.grouped_masked(bytes_of(q), s.cpu().numpy(), bytes_of(qw1), sw1.cpu().numpy(), om)
+    ref2 = oracle.grouped_masked(bytes_of(r["qh"]), r["sh"].cpu().numpy(), bytes_of(qw2), sw2.cpu().numpy(), om)
+    for e in range(E):
+        m = int(om[e])
+        assert_gemm_close(bf16_bits_of(c1)[e, :m], ref1[e, :m], "GEMM1")
+        assert_gemm_close(bf16_bits_of(y)[e, :m], ref2[e, :m], "GEMM2")
+    yf = moe.bf16_to_f32(bf16_bits_of(y)).astype(np.float64).reshape(E * cap, D)
+    ref, mag = moe.combine(yf, osl, r["w"].double().cpu().numpy())
+    err = np.abs(moe.bf16_to_f32(bf16_bits_of(r["out"])).astype(np.float64) - ref)
+    assert np.all(err <= k * U * mag + 2.0 ** -8 * (np.abs(ref) + k * U * mag) + TINY)
+
+
+def test_empty_calls(dev):
+    """No tokens, no rows, no channels: nothing is launched or written, the counts
+    are still set."""
+    e = torch.empty((0, 16), device=dev)
+    ids, w = fq.fp8_moe_route(e, 4)
+    assert ids.shape == w.shape == (0, 4)
+    assert fq.fp8_moe_route_bwd(e, ids, w).shape == (0, 16)
+    counts = torch.full((16,), 7, dtype=torch.int32, device=dev)
+    slots, m, _ = fq.fp8_moe_layout_contiguous(ids, 16, counts=counts)
+    assert slots.shape == (0, 4) and m.numel() == 0 and torch.all(counts == 0)
+    _, mm = fq.fp8_moe_layout_masked(ids, 16, 128)
+    assert torch.all(mm == 0)
+    x = torch.empty((0, 256), dtype=torch.bfloat16, device=dev)
+    q, s = fq.fp8_moe_dispatch_1x128(x, slots, 0, m_indices=m, counts=counts)
+    assert q.shape == (0, 256) and s.shape == (0, 2)
+    keep = torch.full((128, 256), 3.0, dtype=torch.bfloat16, device=dev)
+    assert fq.fp8_moe_combine(keep, slots).shape == (0, 256)
+    dy, dw = fq.fp8_moe_combine_bwd(x, torch.zeros_like(keep), slots, w, dy=keep)
+    assert torch.all(keep == 3.0) and dw.shape == (0, 4)
+    none = torch.empty((3, 0), dtype=torch.bfloat16, device=dev)
+    assert fq.fp8_moe_dispatch_1x128(none, torch.zeros((3, 1), dtype=torch.int32, device=dev), 128)[0].shape == (128, 0)
+    (qh, _), (qc, _) = fq.fp8_swiglu_ckpt_1x128(torch.empty((0, 512), dtype=torch.bfloat16, device=dev))
+    assert qh.shape == (0, 256) and qc.shape == (0, 512)
+    dc, (qd, _) = fq.fp8_swiglu_bwd_1x128(x, torch.empty((0, 512), dtype=torch.uint8, device=dev),
+                                          torch.empty((0, 4), device=dev))
+    assert dc.shape == qd.shape == (0, 512)
+    torch.cuda.synchronize(dev)
 
 
 def test_misaligned_tensors_are_refused(dev):
