@@ -850,7 +850,7 @@ static bool bad_tokens(int64_t T, int64_t top_k, int64_t D, int64_t rows) {
 }
 // The contiguous layout's arrays: both or neither, over whole 128-row blocks.
 static int check_layout(const int32_t* m_indices, const int32_t* counts, int64_t E, int64_t rows) {
-  if (!m_indices && !counts) return FP8Q_OK;
+  if (rows == 0 || (!m_indices && !counts)) return FP8Q_OK;  // no rows: m_indices has no elements, and may be NULL
   if (E < 1 || E > kMaxExperts || rows % 128) return FP8Q_ERR_SHAPE;
   if (!m_indices || !counts) return FP8Q_ERR_NULL;
   if (!aligned(m_indices, 4) || !aligned(counts, 4)) return FP8Q_ERR_ALIGN;

@@ -74,18 +74,27 @@ __device__ __forceinline__ float swiglu16_f32x2(const uint32_t (&gw)[8], const u
   const bool in_range = top <= 0x7B00u && min(least & 0xFFFFu, least >> 16) >= 0x0E00u && g_max < 0x1p+126f;
   if (any == 0u && in_range) return __uint_as_float(top << 16);
   uint32_t redo = 0u;  // bit 2i + j: half j of word i
+  if (in_range) {      // the usual case: only what the bracket left open
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t x = ((d[i] & 0x7FFF7FFFu) + 0x7FFF7FFFu) | d[i];  // bits 15 and 31: halves that differ
+      redo |= ((x >> 15) & 1u) << (2 * i) | (x >> 31) << (2 * i + 1);
+    }
+  } else {
+    const bool all = !(g_max < 0x1p+126f);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t m = (hw[i] >> (16 * j)) & 0x7FFFu;
-      // a zero factor makes an exact zero
-      const bool zero = ((gw[i] >> (16 * j)) & 0x7FFFu) == 0u || ((uw[i] >> (16 * j)) & 0x7FFFu) == 0u;
-      const bool open = ((d[i] >> (16 * j)) & 0xFFFFu) != 0u || ((m < 0x0E00u || m > 0x7B00u) && !zero);
-      redo |= static_cast<uint32_t>(open) << (2 * i + j);
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t m = (hw[i] >> (16 * j)) & 0x7FFFu;
+        const uint32_t g = (gw[i] >> (16 * j)) & 0x7FFFu, u = (uw[i] >> (16 * j)) & 0x7FFFu;
+        // a zero factor makes an exact zero, and rows that nobody wrote (not finite) are not worth the time
+        const bool worth = g != 0u && u != 0u && max(g, u) < 0x7F80u;
+        const bool open = all || ((d[i] >> (16 * j)) & 0xFFFFu) != 0u || m < 0x0E00u || m > 0x7B00u;
+        redo |= static_cast<uint32_t>(open && worth) << (2 * i + j);
+      }
     }
   }
-  if (!(g_max < 0x1p+126f)) redo = 0xFFFFu;
   for (; redo != 0u; redo &= redo - 1u) {
     const int b = __ffs(redo) - 1, i = b >> 1, sh = (b & 1) * 16;
     const uint32_t g = __ldg(reinterpret_cast<const uint32_t*>(gp) + i) >> sh << 16;
@@ -104,11 +113,10 @@ __device__ __forceinline__ float swiglu16_f32x2(const uint32_t (&gw)[8], const u
 //   qc [rows, 2 inter], sc    the tiles of c1 itself, as
 //                             quant_act_1x128_kernel writes them.
 // One pass over c1 instead of two.  Eight lanes own one tile of h and the gate
-// and up tiles it comes from.  Bound by instruction issue (about 630 a warp for
+// and up tiles it comes from.  Bound by instruction issue (about 600 a warp for
 // 512 elements of h, a fifth of them packed FP32, which take two slots): 35072 x
-// 2048 take 115 us on a B200, 4.4 TB/s, 78 us for their bytes at a copy's rate.
-// (With quantize16 and swiglu16 185 us; 48 or 80 registers, shared scales and
-// halfword-integer maxima all within 5% or slower.)
+// 2048 take 110 us on a B200, 4.6 TB/s, 78 us for their bytes at a copy's rate.
+// (With quantize16 and swiglu16 185 us; 48 or 80 registers 117 and 112.)
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256, 4) swiglu_ckpt_1x128_kernel(const uint8_t* __restrict__ c1,
                                                                    uint8_t* __restrict__ qh, float* __restrict__ sh,

@@ -50,6 +50,24 @@ def test_swiglu_checkpoint(dev, rows, inter):
     assert torch.equal(qc.view(torch.uint8), q3.view(torch.uint8)) and torch.equal(sc, s3)
 
 
+def test_swiglu_checkpoint_beside_rows_that_are_not_finite(dev):
+    """Rows of NaN and infinities (blocks that nobody wrote) do not touch their
+    neighbours' tiles."""
+    rng = np.random.default_rng(8)
+    c1 = _c1(rng, 40, 256)
+    bad = c1.copy()
+    bad[5] = 0x7FC0
+    bad[17, ::3] = 0x7F80
+    bad[39] = 0xFF80
+    good = [r for r in range(40) if r not in (5, 17, 39)]
+    (qh, sh), (qc, sc) = fq.fp8_swiglu_ckpt_1x128(to_torch_bf16(bad, dev))
+    torch.cuda.synchronize(dev)
+    oq, os_ = oracle.quant_act_1x128(oracle.swiglu_bf16(c1))
+    assert np.array_equal(bytes_of(qh)[good], oq[good]) and np.array_equal(sh.cpu().numpy()[good], os_[good])
+    oq, os_ = oracle.quant_act_1x128(c1)
+    assert np.array_equal(bytes_of(qc)[good], oq[good]) and np.array_equal(sc.cpu().numpy()[good], os_[good])
+
+
 def _check_tiles(q, s, d, err):
     """q, s quantize values within err of d (float64): s within the error of the tile's amax (and its own
     rounding), every code that of a value within err."""

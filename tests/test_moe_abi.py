@@ -70,6 +70,8 @@ CASES = [
     ("fp8_moe_dispatch_1x128", (A16, 4, 128, A16, 2, 200, A16, A16, 8, A16, A16, None), fq.ERR_SHAPE),
     ("fp8_moe_dispatch_1x128", (A16, 4, 128, A16, 2, 256, A16, A16, 0, A16, A16, None), fq.ERR_SHAPE),
     ("fp8_moe_dispatch_1x128", (A16, 4, 128, A16, 2, 256, A16, None, 8, A16, A16, None), fq.ERR_NULL),
+    ("fp8_moe_dispatch_1x128", (A16, 0, 128, None, 2, 0, None, A16, 8, None, None, None), fq.OK),  # an empty layout
+    ("fp8_moe_combine_bwd", (A16, None, 0, 128, A16, A16, 0, 2, None, A16, 8, None, A16, None), fq.OK),
     ("fp8_moe_dispatch_1x128", (A16, 0, 128, None, 2, 256, None, None, 0, None, None, None), fq.OK),
     ("fp8_moe_dispatch_1x128", (A16, 4, 128, A16, 2, 0, None, None, 0, None, None, None), fq.OK),
     ("fp8_moe_dispatch_1x128", (A16, 4, 128, None, 2, 256, None, None, 0, A16, A16, None), fq.ERR_NULL),
