@@ -1103,7 +1103,7 @@ int fp8_ckpt_128x1_t(const uint8_t* q, const float* s, int64_t M, int64_t K, int
   int rc = device_info(&dev);
   if (rc) return rc;
   const int64_t grid = (Mp / 128) * (K / kCkptChannels);
-  ckpt_128x1_t_kernel<<<static_cast<unsigned>(grid), 128, 0, stream>>>(q, s, qt, st, M, K, Mp);
+  ckpt_128x1_t_kernel<<<static_cast<unsigned>(grid), kCkptThreads, 0, stream>>>(q, s, qt, st, M, K, Mp);
   return launched();
 }
 

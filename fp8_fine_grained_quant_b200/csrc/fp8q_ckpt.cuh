@@ -294,62 +294,63 @@ __global__ void __launch_bounds__(256, 4) swiglu_bwd_1x128_kernel(const uint8_t*
 // v = fl32(code * s) are regrouped along tokens: st = fl32(amax / 448) (1 when
 // 0), codes E4M3(fl32(v / st)).
 //
-// A 128-thread CTA takes 128 tokens x 64 channels: thread t owns channels
-// 8 (t % 8) .. +7 of tokens 8 (t / 8) .. +7 and keeps their 64 values in
+// A 256-thread CTA takes 128 tokens x 64 channels: thread t owns channels
+// 4 (t % 16) .. +3 of tokens 8 (t / 16) .. +7 and keeps their 32 values in
 // registers.  The per-channel maxima are combined over the CTA, one thread per
 // channel computes its scale and reciprocal, every thread quantizes its values
 // (codes by the corrected quotient, a scale a column), and the code bytes are
 // transposed in registers and through a swizzled shared tile, to leave as full
 // 128-byte rows.  Half a block of channels a CTA keeps five CTAs on an SM and
-// the last wave short.  4096 x 7168 take 18.8 us on a B200 (3.2 TB/s; 9.3 us for
-// the bytes), bound by instruction issue and the five waves of 740 CTAs; with an
-// IEEE division an element 51 us, persistent with the next unit copied ahead
-// 18.9.
+// the last wave short.  4096 x 7168 take 18.3 us on a B200 (3.3 TB/s; 9.3 us for
+// the bytes), bound by instruction issue and the five waves of 740 CTAs; with 64
+// values a thread 18.8, with four CTAs an SM 19.7 and with six, which spill, 18.8.
+// With an IEEE division an element 51 us.
 // ---------------------------------------------------------------------------
 constexpr int kCkptChannels = 64;
+constexpr int kCkptThreads = 256;
 
-__global__ void __launch_bounds__(128, 5) ckpt_128x1_t_kernel(const uint8_t* __restrict__ q,
-                                                              const float* __restrict__ s, uint8_t* __restrict__ qt,
-                                                              float* __restrict__ st, int64_t M, int64_t K,
-                                                              int64_t Mp) {
+__global__ void __launch_bounds__(kCkptThreads, 5) ckpt_128x1_t_kernel(const uint8_t* __restrict__ q,
+                                                                       const float* __restrict__ s,
+                                                                       uint8_t* __restrict__ qt,
+                                                                       float* __restrict__ st, int64_t M, int64_t K,
+                                                                       int64_t Mp) {
   __shared__ __align__(16) uint8_t tile[kCkptChannels * 128];
-  __shared__ __align__(16) float col_max[4][kCkptChannels];
+  __shared__ __align__(16) float col_max[kCkptThreads / 32][kCkptChannels];
   __shared__ __align__(16) float ch_scale[kCkptChannels];
   __shared__ __align__(16) float ch_ny[kCkptChannels];  // -1/s; NaN: the channel takes the division
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cg = tid & 7, rg = tid >> 3;
+  const int cg = tid & 15, rg = tid >> 4;
   const int64_t nkc = K / kCkptChannels;
   const int64_t mb = static_cast<uint32_t>(blockIdx.x) / static_cast<uint32_t>(nkc);
   const int64_t kc = static_cast<uint32_t>(blockIdx.x) - mb * nkc;
   const int64_t tok0 = mb * 128 + rg * 8;
-  uint2 c[8];
+  uint32_t c[8];
   float sr[8];
-  const uint8_t* qp = q + tok0 * K + kc * kCkptChannels + cg * 8;
+  const uint8_t* qp = q + tok0 * K + kc * kCkptChannels + cg * 4;
   const float* sp = s + tok0 * (K >> 7) + (kc >> 1);
   const int left = M - tok0 < 8 ? static_cast<int>(M - tok0) : 8;
 #pragma unroll
   for (int r = 0; r < 8; ++r, qp += K, sp += K >> 7) {
-    c[r] = make_uint2(0u, 0u);
+    c[r] = 0u;
     sr[r] = 1.0f;
     if (r < left) {
-      c[r] = __ldg(reinterpret_cast<const uint2*>(qp));
+      c[r] = __ldg(reinterpret_cast<const uint32_t*>(qp));
       sr[r] = __ldg(sp);
     }
   }
-  uint64_t v[8][4];  // [token][channel pair]
-  float m[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  uint64_t v[8][2];  // [token][channel pair]
+  float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int r = 0; r < 8; r += 2) {
 #pragma unroll
     for (int k = r; k < r + 2; ++k) {
       const uint64_t s2 = pack_f32x2(sr[k]);
-      e4m3x4_to_f32x2(c[k].x, v[k][0], v[k][1]);
-      e4m3x4_to_f32x2(c[k].y, v[k][2], v[k][3]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[k][i] = mul_f32x2(v[k][i], s2);
+      e4m3x4_to_f32x2(c[k], v[k][0], v[k][1]);
+      v[k][0] = mul_f32x2(v[k][0], s2);
+      v[k][1] = mul_f32x2(v[k][1], s2);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       float a, b, x, y;
       split_f32x2(v[r][i], a, b);
       split_f32x2(v[r + 1][i], x, y);
@@ -357,21 +358,15 @@ __global__ void __launch_bounds__(128, 5) ckpt_128x1_t_kernel(const uint8_t* __r
       m[2 * i + 1] = max3_abs(m[2 * i + 1], b, y);
     }
   }
-  // lanes l, l ^ 8, l ^ 16 and l ^ 24 hold the same channels (the warp's four token groups)
+  // lanes l and l ^ 16 hold the same channels (the warp's two token groups)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 8));
-    m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 16));
-  }
-  if (lane < 8) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<float4*>(&col_max[warp][cg * 8 + 4 * i]) =
-          make_float4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
-  }
+  for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 16));
+  if (lane < 16) *reinterpret_cast<float4*>(&col_max[warp][cg * 4]) = make_float4(m[0], m[1], m[2], m[3]);
   __syncthreads();
   if (tid < kCkptChannels) {
-    const float a = fmaxf(fmaxf(col_max[0][tid], col_max[1][tid]), fmaxf(col_max[2][tid], col_max[3][tid]));
+    float a = col_max[0][tid];
+#pragma unroll
+    for (int w = 1; w < kCkptThreads / 32; ++w) a = fmaxf(a, col_max[w][tid]);
     const float sv = group_scale_f32(a);
     float y;
     const bool ok = corrected_reciprocal(sv, y);
@@ -380,54 +375,50 @@ __global__ void __launch_bounds__(128, 5) ckpt_128x1_t_kernel(const uint8_t* __r
     st[mb * K + kc * kCkptChannels + tid] = sv;
   }
   __syncthreads();
-  uint64_t ny2[4], s2[4];
-  bool ok = true;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 y = *reinterpret_cast<const float2*>(&ch_ny[cg * 8 + 2 * i]);
-    const float2 x = *reinterpret_cast<const float2*>(&ch_scale[cg * 8 + 2 * i]);
-    ny2[i] = join_f32x2(y.x, y.y);
-    s2[i] = join_f32x2(x.x, x.y);
-    ok = ok && y.x < 0.0f && y.y < 0.0f;
-  }
-  uint32_t clo[8], chi[8];
+  const float4 y4 = *reinterpret_cast<const float4*>(&ch_ny[cg * 4]);
+  const float4 x4 = *reinterpret_cast<const float4*>(&ch_scale[cg * 4]);
+  const uint64_t ny2[2] = {join_f32x2(y4.x, y4.y), join_f32x2(y4.z, y4.w)};
+  const uint64_t s2[2] = {join_f32x2(x4.x, x4.y), join_f32x2(x4.z, x4.w)};
+  const bool ok = y4.x < 0.0f && y4.y < 0.0f && y4.z < 0.0f && y4.w < 0.0f;
+  uint32_t code[8];  // token r's four channels
   if (ok) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      clo[r] = e4m3x4_from_f32x2(neg_quotient(v[r][0], ny2[0], s2[0]), neg_quotient(v[r][1], ny2[1], s2[1])) ^
-               0x80808080u;
-      chi[r] = e4m3x4_from_f32x2(neg_quotient(v[r][2], ny2[2], s2[2]), neg_quotient(v[r][3], ny2[3], s2[3])) ^
-               0x80808080u;
-    }
+    for (int r = 0; r < 8; ++r)
+      code[r] = e4m3x4_from_f32x2(neg_quotient(v[r][0], ny2[0], s2[0]), neg_quotient(v[r][1], ny2[1], s2[1])) ^
+                0x80808080u;
   } else {
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      uint64_t d[4];
+      uint64_t d[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         float a, b, x, y;
         split_f32x2(v[r][i], a, b);
         split_f32x2(s2[i], x, y);
         d[i] = join_f32x2(__fdiv_rn(a, x), __fdiv_rn(b, y));
       }
-      clo[r] = e4m3x4_from_f32x2(d[0], d[1]);
-      chi[r] = e4m3x4_from_f32x2(d[2], d[3]);
+      code[r] = e4m3x4_from_f32x2(d[0], d[1]);
     }
   }
-  transpose8x8_bytes(clo, chi);  // now channel i: tokens 0-3 in clo[i], 4-7 in chi[i]
-  // channel row cg*8 + i of the tile, logical 8-byte slot rg, physical slot rg ^ 2cg: a
-  // half warp's sixteen stores fall in sixteen slots
+  // now channel i: tokens 0-3 in code[i], 4-7 in code[4 + i]
+  transpose4x4_bytes(code[0], code[1], code[2], code[3]);
+  transpose4x4_bytes(code[4], code[5], code[6], code[7]);
+  // channel row cg*4 + i of the tile, logical 8-byte slot rg, physical slot rg ^ cg: a half
+  // warp's sixteen stores fall in sixteen slots
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<uint2*>(tile + (cg * 8 + i) * 128 + ((rg ^ (2 * cg)) << 3)) = make_uint2(clo[i], chi[i]);
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint2*>(tile + (cg * 4 + i) * 128 + ((rg ^ cg) << 3)) = make_uint2(code[i], code[4 + i]);
   __syncthreads();
   uint8_t* dst = qt + kc * kCkptChannels * Mp + mb * 128;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = (tid >> 3) + 16 * i, ch = tid & 7;
-    // logical slots 2ch and 2ch + 1 sit in physical 16-byte chunk ch ^ (row / 8)
-    *reinterpret_cast<uint4*>(dst + row * Mp + ch * 16) =
-        *reinterpret_cast<const uint4*>(tile + row * 128 + ((ch ^ (row >> 3)) << 4));
+  for (int i = 0; i < 2; ++i) {
+    const int row = (tid >> 3) + 32 * i, ch = tid & 7;
+    const int swz = row >> 2;
+    // logical slots 2ch and 2ch + 1 sit in physical 16-byte chunk ch ^ (swz / 2), their
+    // halves swapped when swz is odd
+    uint4 o = *reinterpret_cast<const uint4*>(tile + row * 128 + ((ch ^ (swz >> 1)) << 4));
+    if (swz & 1) o = make_uint4(o.z, o.w, o.x, o.y);
+    *reinterpret_cast<uint4*>(dst + row * Mp + ch * 16) = o;
   }
 }
 

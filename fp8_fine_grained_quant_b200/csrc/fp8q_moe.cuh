@@ -767,8 +767,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_bwd_kernel(RouteBw
 // ranks, from registers where a run is short.  One launch and no atomics.  For
 // many entries a launch before it counts the experts of each chunk into a
 // workspace, and the CTAs of this one, no cluster, sum those.  On a B200: 4.9 us
-// for 488 entries, 8.1 for 32768 (latency: barriers and a few hundred dependent
-// steps), 13.5 for 262144.
+// for 488 entries, 8.0 for 32768 (latency: barriers and a few hundred dependent
+// steps), 11 to 12.5 for 262144.
 // ---------------------------------------------------------------------------
 struct LayoutArgs {
   const int32_t* ids;
@@ -784,7 +784,8 @@ struct LayoutArgs {
 
 // Above this many entries eight SMs are too few for them: the layout takes two
 // launches, a CTA per kLayoutChunk entries, and a workspace.  (32768 entries: 8.1
-// us in one cluster, 8.9 in two launches; 262144: 58 against 13.5.)
+// us in one cluster, 8.9 in two launches; 262144: 58 against 13.5, when both were
+// measured.)
 constexpr int64_t kLayoutClusterMax = 32768;
 constexpr int kLayoutChunk = 4096;
 
