@@ -912,7 +912,7 @@ int fp8_moe_route_bwd(const void* logits, int logits_bf16, int64_t T, int64_t E,
 int64_t fp8_moe_layout_workspace(int64_t T, int64_t top_k, int64_t E) {
   if (bad_topk(T, top_k) || E < 1 || E > kMaxExperts) return 0;
   const int64_t n = T * top_k;
-  return n <= kLayoutClusterMax ? 0 : (n + kLayoutChunk - 1) / kLayoutChunk * E;
+  return n <= kLayoutClusterMax ? 0 : layout_chunks(n) * E;
 }
 
 static int run_layout(LayoutArgs a, cudaStream_t stream) {
@@ -923,8 +923,9 @@ static int run_layout(LayoutArgs a, cudaStream_t stream) {
   int rc = device_info(&dev);
   if (rc) return rc;
   if (a.n > kLayoutClusterMax) {
-    const unsigned chunks = static_cast<unsigned>((a.n + kLayoutChunk - 1) / kLayoutChunk);
-    moe_layout_count_kernel<<<chunks, kLayoutThreads, 0, stream>>>(a.ids, a.n, a.E, a.chunk_counts);
+    const unsigned chunks = static_cast<unsigned>(layout_chunks(a.n));
+    const int64_t chunk = layout_groups(a.n, chunks) * kLayoutThreads;  // entries of a CTA
+    moe_layout_count_kernel<<<chunks, kLayoutThreads, 0, stream>>>(a.ids, a.n, chunk, a.E, a.chunk_counts);
     rc = launched();
     if (rc) return rc;
     moe_layout_kernel<<<chunks, kLayoutThreads, layout_smem(a.E), stream>>>(a);

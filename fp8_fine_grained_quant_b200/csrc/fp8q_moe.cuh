@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_bwd_kernel(RouteBw
 // many entries a launch before it counts the experts of each chunk into a
 // workspace, and the CTAs of this one, no cluster, sum those.  On a B200: 4.9 us
 // for 488 entries, 8.0 for 32768 (latency: barriers and a few hundred dependent
-// steps), 11 to 12.5 for 262144.
+// steps), 11 to 13 for 262144, 104 for 8388608.
 // ---------------------------------------------------------------------------
 struct LayoutArgs {
   const int32_t* ids;
@@ -783,17 +783,29 @@ struct LayoutArgs {
 };
 
 // Above this many entries eight SMs are too few for them: the layout takes two
-// launches, a CTA per kLayoutChunk entries, and a workspace.  (32768 entries: 8.1
-// us in one cluster, 8.9 in two launches; 262144: 58 against 13.5, when both were
-// measured.)
+// launches, a CTA per kLayoutChunk entries or, from one CTA an SM on, per equal
+// share of them (every CTA sums all CTAs' counts, so more CTAs cost their
+// square: 8388608 entries of 256 experts take 104 us in 148 shares, 1000 in
+// chunks of 4096), and a workspace.  (32768 entries: 8.1 us in one cluster, 8.9 in two
+// launches; 262144: 58 against 13.5, when both were measured.)
 constexpr int64_t kLayoutClusterMax = 32768;
 constexpr int kLayoutChunk = 4096;
+constexpr int kLayoutMaxChunks = 148;
+constexpr int64_t layout_chunks(int64_t n) {
+  const int64_t c = (n + kLayoutChunk - 1) / kLayoutChunk;
+  return c < kLayoutMaxChunks ? c : kLayoutMaxChunks;
+}
 
 constexpr int kLayoutThreads = 1024;
 constexpr int kLayoutWarps = kLayoutThreads / 32;
 constexpr int kLayoutMaxCtas = 8;  // the portable cluster size
 constexpr int kLayoutAhead = 4;    // groups of 32 entries loaded together
 constexpr int layout_smem(int E) { return kLayoutWarps * E * 4; }
+
+// Groups of 32 entries that each warp of `ctas` CTAs takes.
+__host__ __device__ constexpr int64_t layout_groups(int64_t n, int64_t ctas) {
+  return (n + kLayoutThreads * ctas - 1) / (kLayoutThreads * ctas);
+}
 
 // The lanes that hold the same id; `bits` covers every id and -1.
 __device__ __forceinline__ uint32_t same_lanes(int e, int bits) {
@@ -806,23 +818,28 @@ __device__ __forceinline__ uint32_t same_lanes(int e, int bits) {
   return same;
 }
 
-// First launch of a large layout: the entries of each expert in each chunk
-// (integer shared-memory atomics: their order does not change a count).
+// First launch of a large layout: the entries of each expert in each chunk of
+// `chunk` entries (integer shared-memory atomics: their order does not change a
+// count).
 __global__ void __launch_bounds__(kLayoutThreads) moe_layout_count_kernel(const int32_t* __restrict__ ids, int64_t n,
-                                                                          int32_t E, int32_t* __restrict__ counts) {
+                                                                          int64_t chunk, int32_t E,
+                                                                          int32_t* __restrict__ counts) {
   __shared__ int32_t hist[kMaxExperts];
   const int tid = threadIdx.x;
   hist[tid] = 0;
   __syncthreads();
-  int e[kLayoutChunk / kLayoutThreads];
+  const int64_t from = blockIdx.x * chunk, to = from + chunk < n ? from + chunk : n;
+  for (int64_t i0 = from + tid; i0 < to; i0 += kLayoutChunk) {
+    int e[kLayoutChunk / kLayoutThreads];
 #pragma unroll
-  for (int k = 0; k < kLayoutChunk / kLayoutThreads; ++k) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kLayoutChunk + k * kLayoutThreads + tid;
-    e[k] = i < n ? __ldg(ids + i) : -1;
+    for (int k = 0; k < kLayoutChunk / kLayoutThreads; ++k) {
+      const int64_t i = i0 + k * kLayoutThreads;
+      e[k] = i < to ? __ldg(ids + i) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kLayoutChunk / kLayoutThreads; ++k)
+      if (static_cast<uint32_t>(e[k]) < static_cast<uint32_t>(E)) atomicAdd(&hist[e[k]], 1);
   }
-#pragma unroll
-  for (int k = 0; k < kLayoutChunk / kLayoutThreads; ++k)
-    if (static_cast<uint32_t>(e[k]) < static_cast<uint32_t>(E)) atomicAdd(&hist[e[k]], 1);
   __syncthreads();
   if (tid < E) counts[static_cast<int64_t>(blockIdx.x) * E + tid] = hist[tid];
 }
@@ -838,8 +855,7 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(LayoutArgs a
   const int E = a.E, bits = 33 - __clz(E - 1);  // of the ids below E, and one that only -1 has
   int32_t* mine = layout_table + warp * E;
   // groups of 32 entries of a warp, its first entry, and the CTA's warps that have any
-  const int64_t per_cta = kLayoutWarps * 32 * static_cast<int64_t>(gridDim.x);
-  const int64_t groups = (a.n + per_cta - 1) / per_cta;
+  const int64_t groups = layout_groups(a.n, gridDim.x);
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * kLayoutWarps + warp) * groups * 32 + lane;
   const int64_t left = a.n - static_cast<int64_t>(blockIdx.x) * kLayoutWarps * groups * 32;
   const int warps = left <= 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(kLayoutWarps),

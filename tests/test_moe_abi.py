@@ -189,6 +189,7 @@ def test_layout_workspace_size():
     ws = fq.lib().fp8_moe_layout_workspace
     assert ws(4096, 8, 32) == 0                       # one cluster
     assert ws(4097, 8, 32) == 9 * 32                  # 32776 entries: nine chunks of 4096
+    assert ws(1 << 20, 8, 256) == 148 * 256           # no more chunks than SMs
     assert ws(-1, 8, 32) == ws(4097, 33, 32) == ws(4097, 8, 1025) == 0
 
 

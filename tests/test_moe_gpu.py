@@ -289,6 +289,22 @@ def test_layout_of_many_entries(dev):
         assert np.array_equal(counts.cpu().numpy(), oc)
 
 
+@pytest.mark.parametrize("T,k,E", [(606208, 1, 40), (606209, 1, 1), (75777, 8, 1024), (200001, 8, 33)])
+def test_layout_of_more_entries_than_a_chunk_an_sm(dev, T, k, E):
+    """From 148 chunks of 4096 entries on the chunks grow; the last may be short or empty."""
+    rng = np.random.default_rng(T)
+    ids = rng.integers(-1, E, (T, k)).astype(np.int32)
+    t = torch.from_numpy(ids).to(dev)
+    slots, m, counts = fq.fp8_moe_layout_contiguous(t, E)
+    os_, om, oc = moe.layout_contiguous(ids, E)
+    assert np.array_equal(slots.cpu().numpy(), os_) and np.array_equal(m.cpu().numpy(), om)
+    assert np.array_equal(counts.cpu().numpy(), oc)
+    cap = (T * k // (E + 1)) // 128 * 128 + 128
+    slots, mm = fq.fp8_moe_layout_masked(t, E, cap)
+    os_, om = moe.layout_masked(ids, E, cap)
+    assert np.array_equal(slots.cpu().numpy(), os_) and np.array_equal(mm.cpu().numpy(), om)
+
+
 def test_large_layout_on_another_stream(dev):
     """The workspace of a large layout belongs to the stream the call names: two
     streams at once, each with its own entries, repeated."""
