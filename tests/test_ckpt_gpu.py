@@ -260,3 +260,29 @@ def test_expert_mlp_training_step(dev):
     assert np.array_equal(bytes_of(qxt), oqt) and np.array_equal(sxt.cpu().numpy(), ost)
     ref = oracle.gemm_1d1d(bytes_of(qdt), sdt.cpu().numpy().T.copy(), oqt, ost.T.copy())
     assert_gemm_close(bf16_bits_of(dw1), ref, "Wgrad1")
+
+
+def test_offsets_beyond_32_bits(dev):
+    """Element offsets that pass 2^32: the last rows of large operands give what
+    the same rows give alone."""
+    inter, n = 7168, 512
+    rows = 300_544                       # rows * 2 * inter > 2^32
+    assert (rows - n) * 2 * inter > 1 << 32
+    c1 = torch.zeros((rows, 2 * inter), dtype=torch.bfloat16, device=dev)
+    c1[-n:] = torch.randn((n, 2 * inter), dtype=torch.bfloat16, device=dev)
+    (qh, sh), (qc, sc) = fq.fp8_swiglu_ckpt_1x128(c1)
+    (qhn, shn), (qcn, scn) = fq.fp8_swiglu_ckpt_1x128(c1[-n:])
+    del c1
+    for big, small in ((qh, qhn), (sh, shn), (qc, qcn), (sc, scn)):
+        assert torch.equal(big[-n:].view(torch.uint8), small.view(torch.uint8))
+    assert int(qc[:-n].view(torch.uint8).count_nonzero()) == 0 and bool((sc[:-n] == 1).all())
+    dh = torch.randn((rows, inter), dtype=torch.bfloat16, device=dev)
+    dc, (q, s) = fq.fp8_swiglu_bwd_1x128(dh, qc, sc)
+    dcn, (qn, sn) = fq.fp8_swiglu_bwd_1x128(dh[-n:], qcn, scn)
+    assert torch.equal(dc[-n:], dcn) and torch.equal(q[-n:].view(torch.uint8), qn.view(torch.uint8))
+    assert torch.equal(s[-n:], sn)
+    del dc, dh
+    qt, st = fq.fp8_ckpt_128x1_t(q, s, Mp=rows)
+    qtn, stn = fq.fp8_ckpt_128x1_t(qn, sn, Mp=n)
+    assert torch.equal(qt[:, -n:].contiguous().view(torch.uint8), qtn.view(torch.uint8))
+    assert torch.equal(st[-(n // 128):], stn)

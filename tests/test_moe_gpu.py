@@ -590,3 +590,45 @@ def test_results_do_not_depend_on_the_run(dev):
         got = (bytes_of(dy), bytes_of(dw), bytes_of(fq.fp8_moe_combine(y, slots, w)))
         first = first or got
         assert all(np.array_equal(a, b) for a, b in zip(first, got))
+
+
+def test_offsets_beyond_32_bits(dev):
+    """Rows whose byte and element offsets pass 2^32: the last rows of large buffers get
+    what the same rows give in small ones."""
+    T, k, D = 40, 2, 7168
+    rows = 600_064                       # rows * D > 2^32
+    assert (rows - 128) * D > 1 << 32
+    rng = np.random.default_rng(5)
+    slots = torch.from_numpy(rng.permutation(T * k).astype(np.int32).reshape(T, k)).to(dev)   # in the last 128 rows
+    far = slots + (rows - 128)
+    x = torch.randn((T, D), dtype=torch.bfloat16, device=dev)
+    q, s = torch.zeros((rows, D), dtype=torch.uint8, device=dev), torch.zeros((rows, D // 128), device=dev)
+    fq.fp8_moe_dispatch_1x128(x, far, rows, q=q, s=s)
+    qn, sn = torch.zeros((128, D), dtype=torch.uint8, device=dev), torch.zeros((128, D // 128), device=dev)
+    fq.fp8_moe_dispatch_1x128(x, slots, 128, q=qn, s=sn)
+    assert torch.equal(q[-128:], qn) and torch.equal(s[-128:], sn)
+    assert int(q[:-128].count_nonzero()) == 0 and int(s[:-128].count_nonzero()) == 0
+    del q, s
+    y = torch.zeros((rows, D), dtype=torch.bfloat16, device=dev)
+    y[-128:] = torch.randn((128, D), dtype=torch.bfloat16, device=dev)
+    w = torch.rand((T, k), device=dev)
+    assert torch.equal(fq.fp8_moe_combine(y, far, w), fq.fp8_moe_combine(y[-128:], slots, w))
+    dy, dyn = torch.zeros_like(y), torch.zeros((128, D), dtype=torch.bfloat16, device=dev)
+    _, dw = fq.fp8_moe_combine_bwd(x, y, far, w, dy=dy)
+    _, dwn = fq.fp8_moe_combine_bwd(x, y[-128:], slots, w, dy=dyn)
+    assert torch.equal(dw, dwn) and torch.equal(dy[-128:], dyn) and int(dy[:-128].count_nonzero()) == 0
+
+
+def test_logits_beyond_32_bits(dev):
+    """T * E passes 2^32: the last rows' choice, weights and gradients."""
+    E, k = 1024, 8
+    T = (1 << 22) + 300
+    logits = torch.zeros((T, E), dtype=torch.bfloat16, device=dev)
+    logits[-300:] = torch.randn((300, E), dtype=torch.bfloat16, device=dev)
+    ids, w = fq.fp8_moe_route(logits, k)
+    ids0, w0 = fq.fp8_moe_route(logits[-300:], k)
+    assert torch.equal(ids[-300:], ids0) and torch.equal(w[-300:], w0)
+    assert bool((ids[:-300] == torch.arange(k, dtype=torch.int32, device=dev)).all())   # ties: the lower index
+    g = torch.randn((T, k), device=dev)
+    d = fq.fp8_moe_route_bwd(logits, ids, g, renorm=False)
+    assert torch.equal(d[-300:], fq.fp8_moe_route_bwd(logits[-300:], ids0, g[-300:], renorm=False))
