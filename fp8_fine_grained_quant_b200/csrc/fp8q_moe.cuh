@@ -328,6 +328,34 @@ __device__ __forceinline__ void share_values(const uint32_t (&w)[VPL], bool vect
   }
 }
 
+// FP32 scores of the choice, and how far their keys may be off: key_reach is the
+// least distance at which the keys a and b are surely in order.
+template <bool kSigmoid>
+__device__ __forceinline__ float score_f32(float l, float row_max, float inv_sum) {
+  return kSigmoid ? rcp_approx(1.0f + exp_approx(-l)) : exp_approx(l - row_max) * inv_sum;
+}
+template <bool kSigmoid>
+__device__ __forceinline__ float key_reach(float a, float b) {
+  return (kSigmoid ? 0x1p-20f : 0x1p-17f) + 0x1p-22f * fmaxf(fabsf(a), fabsf(b));
+}
+
+// Whether every expert in [from, end) of the warp's lanes whose key lies in reach
+// of expert `last`'s has its very logit and bias.  Out of line: few rows need it.
+template <bool kBf16, bool kSigmoid>
+__device__ __noinline__ bool border_is_equal(const void* row, const float* bias, int from, int end, int last,
+                                             float row_max, float inv_sum) {
+  const float ll = load_logit<kBf16>(row, last), lb = __ldg(bias + last);
+  const float lk = score_f32<kSigmoid>(ll, row_max, inv_sum) + lb;
+  bool equal = true;
+  for (int e = from; e < end; ++e) {
+    const float l = load_logit<kBf16>(row, e), b = __ldg(bias + e);
+    if (!(l > neg_inf_f32() && b > neg_inf_f32())) continue;  // never chosen
+    const float k = score_f32<kSigmoid>(l, row_max, inv_sum) + b;
+    equal = equal && ((l == ll && b == lb) || fabsf(k - lk) > key_reach<kSigmoid>(k, lk));
+  }
+  return __all_sync(0xFFFFFFFFu, equal);
+}
+
 constexpr int kExactVpl = 8;  // up to this share, a comparison that FP32 leaves open is settled in registers
 constexpr int kRouteWarps = 4;
 constexpr int kRouteCtasPerSm = 8;  // up to eight experts a lane: 64 registers
@@ -342,11 +370,12 @@ constexpr int kRouteCtasPerSm = 8;  // up to eight experts a lane: 64 registers
 // for group sums, FP32 keys are compared, and each comparison that decides
 // (neighbours in the choice, the first expert left out, the worst group kept
 // against the best one dropped) must be wider than the keys' error.  Equal keys
-// of equal logits and biases need no proof.  Where one is not (about one row in
-// a thousand), the keys within reach of the comparison are evaluated in
-// binary64, a key a lane: the best of every group, or the chosen and those next
-// to the last of them.  Shares above eight experts, and more than 32 keys in
-// reach, take route_choose_f64.
+// of equal logits and biases need no proof among the chosen; where the first one
+// left out equals the last chosen, every key in reach must (border_is_equal).
+// Where one is not (about one row in a thousand), the keys within reach of the
+// comparison are evaluated in binary64, a key a lane: the best of every group, or
+// the chosen and those next to the last of them.  Shares above eight experts, and
+// more than 32 keys in reach, take route_choose_f64.
 //
 // Bound by instruction issue (about 790 a row of 256 experts, half of them on the
 // integer and compare pipe), not by its bytes: 32768 rows of 256 experts in 8
@@ -405,9 +434,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
       row_sum = warp_sum(row_sum);
     }
     const float inv_sum = rcp_approx(row_sum);
-    auto score = [&](float x) {
-      return kSigmoid ? rcp_approx(1.0f + exp_approx(-x)) : exp_approx(x - row_max) * inv_sum;
-    };
+    auto score = [&](float x) { return score_f32<kSigmoid>(x, row_max, inv_sum); };
 
     // keys: the logits (-0 as +0), or score + bias; -inf: never chosen
     float key[VPL], s[VPL];
@@ -431,6 +458,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
     sort_descending<VPL>(s);
 
     bool certain = true;
+    bool stays = true;  // the lane's group is kept
     if (a.n_group > 1) {
       // the group's best one or two, in every lane of the group
       float b1 = s[0], b2 = VPL > 1 ? s[VPL > 1 ? 1 : 0] : neg_inf_f32();
@@ -501,6 +529,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
           }
         }
       }
+      stays = keep;
       if (!keep) s[0] = neg_inf_f32();  // the lane never gives up a key
     }
 
@@ -554,12 +583,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
       if (lane == 31) next = rest;
       bool sure = true;
       if (lane < a.top_k && next > neg_inf_f32())
-        sure = my_key - next > tol + 0x1p-22f * fmaxf(fabsf(my_key), fabsf(next));
+        sure = my_key - next > key_reach<kSigmoid>(my_key, next);
       if (certain && !__all_sync(0xFFFFFFFFu, sure)) {
         // keys in one another's reach: certain only between equal logits with equal biases
         float bid = id >= 0 ? __ldg(a.bias + id) : 0.0f;
         const float nl = __shfl_down_sync(0xFFFFFFFFu, lid, 1), nb = __shfl_down_sync(0xFFFFFFFFu, bid, 1);
         certain = __all_sync(0xFFFFFFFFu, sure || (lane < 31 && lid == nl && bid == nb));
+        if (certain && !((__ballot_sync(0xFFFFFFFFu, sure) >> (a.top_k - 1)) & 1u)) {
+          // the first expert left out equals the last chosen, so it stands for none of those behind it
+          const int end = stays ? base + count : base;
+          certain = border_is_equal<kBf16, kSigmoid>(row, a.bias, base, end, __shfl_sync(0xFFFFFFFFu, id, a.top_k - 1),
+                                                     row_max, inv_sum);
+        }
         if (VPL <= kExactVpl && !certain && a.top_k < 32) {
           // more places, until the next key cannot reach the last that counts
           const float kth = __shfl_sync(0xFFFFFFFFu, my_key, a.top_k - 1);
