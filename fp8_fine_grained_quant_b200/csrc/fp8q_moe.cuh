@@ -389,7 +389,9 @@ constexpr int kRouteCtasPerSm = 8;  // up to eight experts a lane: 64 registers
 //            sum p |x| <= ln 1024), and 3 * 2^-23: below 2^-17.9 for any two
 //            keys, as their p sum to at most 1;
 // so two keys further apart than 2^-20 (sigmoid) or 2^-17 (softmax) + 2^-22 of
-// the larger are in order; for sums of two keys, twice that.
+// the larger are in order, and a sum of two keys is off by at most that tolerance
+// and 2^-20 of its larger key (2^-22 from both keys, 2^-23 from the sum and from
+// adding the bound to it).
 template <int VPL, bool kBf16, bool kSigmoid, bool biased>
 __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm : 1)
     moe_route_kernel(RouteArgs a, RouteSplit sp) {
@@ -468,9 +470,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
         b1 = fmaxf(b1, o1);
       }
       float total = b1;  // group_top 1: the best key decides
+      float mag = fabsf(b1);  // the largest magnitude in it (of a sum of scores, which do not cancel, below 1)
       if (pair_sums) {
         const float v1 = biased ? b1 : score(b1), v2 = biased ? b2 : score(b2);
         total = b1 == neg_inf_f32() ? b1 : (b2 == neg_inf_f32() ? v1 : v1 + v2);
+        mag = biased ? (b2 == neg_inf_f32() ? mag : fmaxf(mag, -b2)) : 1.0f;
       }
       // groups ahead of this one, a share of the comparisons in each of its lanes
       const int lanes = 1 << sp.lanes_log2;
@@ -484,9 +488,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
       const bool in = g < a.n_group;
       bool keep = in && ahead < a.topk_group;
       if ((pair_sums || biased) && a.topk_group < a.n_group) {
-        const float w = redux_min(keep ? total : __int_as_float(0x7F800000));
-        const float b = redux_max(in && !keep ? total : neg_inf_f32());
-        if (!(b == neg_inf_f32() || w - b > 2.0f * tol + 0x1p-20f * fmaxf(fabsf(w), fabsf(b)))) {
+        // each total's least and largest possible value: it is off by as much as its keys are, and they may cancel
+        const float err = tol + 0x1p-20f * mag;
+        const float w = redux_min(keep ? fmaxf(total - err, neg_inf_f32()) : __int_as_float(0x7F800000));
+        const float b = redux_max(in && !keep ? fmaxf(total + err, neg_inf_f32()) : neg_inf_f32());  // NaN: no key
+        if (!(b == neg_inf_f32() || w > b)) {
           if constexpr (VPL <= kExactVpl) {
             // the groups' sums in binary64, of the keys that can be among their best: each lane's
             // next largest in turn while some lane has one

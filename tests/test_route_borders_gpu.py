@@ -1,7 +1,7 @@
 """Borders of the expert choice that FP32 leaves open: the last expert chosen and
-the first one left out are equal and a third key lies within FP32's reach of them.
-The ids must be those of the binary64 keys (oracle/moe.py), whatever the FP32 keys
-say."""
+the first one left out are equal and a third key lies within FP32's reach of them;
+sums of two keys that cancel.  The ids must be those of the binary64 keys
+(oracle/moe.py), whatever the FP32 keys say."""
 import numpy as np
 import pytest
 import torch
@@ -87,3 +87,43 @@ def test_rows_of_equal_logits_go_to_the_lowest_indices(dev, E, k):
     for bias in (np.zeros(E), np.where(np.arange(E) % 3, 0.5, 0.25)):
         for score in ("softmax", "sigmoid"):
             _same_ids(dev, l, k, bias=bias, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,KG", [(32, 4, 2), (256, 8, 4), (60, 5, 1), (1024, 2, 1), (64, 32, 5)])
+@pytest.mark.parametrize("size_of_bias", [4.0, 1000.0, 3e5])
+def test_group_sums_that_cancel(dev, score, E, G, KG, size_of_bias):
+    """The best two keys of each group are + and - a large bias: their FP32 sum is
+    off by the bias's rounding, far more than the sum's."""
+    rng = np.random.default_rng(E + G)
+    size = E // G
+    T = 200
+    bias = np.full(E, -np.inf)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    for g in range(G):
+        a, b = rng.choice(size, 2, replace=False)
+        bias[g * size + a], bias[g * size + b] = size_of_bias, -size_of_bias
+        # sums of two scores that differ between the groups by a few FP32 steps of the bias at most
+        step = 2.0 ** -22 * size_of_bias if size_of_bias < 1e4 else 0.05
+        l[:, g * size + a] = (0.25 + step * rng.standard_normal(T)).astype(np.float32)
+        l[:, g * size + b] = (-0.5 + step * rng.standard_normal(T)).astype(np.float32)
+    _same_ids(dev, l, 2 * KG, bias=bias, score=score, n_group=G, topk_group=KG, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_sums_of_very_large_and_infinite_biases(dev, score):
+    """Sums beyond FP32's largest value, infinite ones, and groups with one expert
+    or none left."""
+    rng = np.random.default_rng(3)
+    E, G, size = 64, 8, 8
+    l = rng.standard_normal((40, E)).astype(np.float32)
+    l[:, 7 * size:] = -np.inf                    # no expert
+    l[::2, 6 * size + 1:7 * size] = -np.inf      # one expert
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    bias[:2] = 3.4e38
+    bias[size:size + 2] = 3.3e38
+    bias[2 * size] = np.inf
+    bias[3 * size:3 * size + 2] = 3.4e38
+    bias[4 * size:4 * size + 2] = -3.4e38
+    for KG in (1, 2, 3, 4, 5, 7, 8):
+        _same_ids(dev, l, 2, bias=bias, score=score, n_group=G, topk_group=KG, group_top=2)
