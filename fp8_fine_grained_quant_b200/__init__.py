@@ -140,7 +140,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(stream, device) -> int:
     if stream is None:
-        if _raw_stream is not None and device.index is not None:
+        if _raw_stream is not None and isinstance(device, torch.device) and device.index is not None:
             return _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
@@ -200,7 +200,6 @@ _I32 = (torch.int32,)
 
 def _p(t):
     return None if t is None else t.data_ptr()  # ctypes makes the pointer (argtypes)
-
 
 
 def _multiple(v: int, name: str):
