@@ -104,30 +104,43 @@ T* ptr(const Opt& t) {
 
 // The call's device, made current, and its stream: None (the device's current
 // stream), a torch.cuda.Stream, or a handle.
+c10::cuda::CUDAStream call_stream(const py::object& s, const c10::cuda::CUDAStream& current) {
+  if (s.is_none()) return current;
+  const auto handle = (py::hasattr(s, "cuda_stream") ? s.attr("cuda_stream") : s).cast<uintptr_t>();
+  if (handle == reinterpret_cast<uintptr_t>(current.stream())) return current;
+  // cudaStreamLegacy is the default stream; as a handle of its own the allocator would take it for a pool's number
+  const auto named = handle == reinterpret_cast<uintptr_t>(cudaStreamLegacy) ? 0 : handle;
+  return c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(named), current.device_index());
+}
+
+// Memory that a call allocates comes from the pool of the stream it runs on: a
+// block of the current stream's pool may have work of that stream queued on it,
+// which another stream would not wait for.
 struct On {
   c10::cuda::CUDAGuard guard;
+  c10::cuda::CUDAStream caller;  // the device's current stream
+  c10::cuda::CUDAStream own;     // the call's
   cudaStream_t stream;
-  On(const Place& p, const py::object& s) : guard(*p.dev) {
-    if (s.is_none())
-      stream = c10::cuda::getCurrentCUDAStream(p.dev->index()).stream();
-    else
-      stream = reinterpret_cast<cudaStream_t>(
-          (py::hasattr(s, "cuda_stream") ? s.attr("cuda_stream") : s).cast<uintptr_t>());
+  On(const Place& p, const py::object& s)
+      : guard(*p.dev),
+        caller(c10::cuda::getCurrentCUDAStream(p.dev->index())),
+        own(call_stream(s, caller)),
+        stream(own.stream()) {}
+  Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
+    if (own == caller) return at::Tensor(at::detail::empty_cuda(shape, type, guard.current_device(), std::nullopt));
+    const c10::cuda::CUDAStreamGuard on_own(own);
+    return at::Tensor(at::detail::empty_cuda(shape, type, guard.current_device(), std::nullopt));
   }
-  // n int32 of scratch for work on this stream only (an undefined tensor for none).  The allocator may hand the
-  // memory out again once it is dropped: to work queued on the device's current stream, or, where the call runs on
-  // another one, after that stream has passed this point.
-  Tensor scratch(int64_t n) const {
-    if (n == 0) return Tensor();
-    Tensor t = at::detail::empty_cuda({n}, at::kInt, guard.current_device(), std::nullopt);
-    const auto index = guard.current_device().index();
-    if (stream != c10::cuda::getCurrentCUDAStream(index).stream())
-      c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(),
-                                                    c10::cuda::getStreamFromExternal(stream, index));
-    return t;
-  }
+  // n int32 of scratch for this call's work (an undefined tensor for none).  Dropped when the call returns, its
+  // memory goes to later work of the same stream.
+  Tensor scratch(int64_t n) const { return n == 0 ? Tensor() : make({n}, at::kInt); }
+  // An output the caller did not pass.  Work that the current stream has queued on it when it is dropped ends before
+  // its memory is handed out again.
   Tensor fresh(const Opt& given, at::IntArrayRef shape, at::ScalarType type) const {
-    return given ? *given : at::Tensor(at::detail::empty_cuda(shape, type, guard.current_device(), std::nullopt));
+    if (given) return *given;
+    Tensor t = make(shape, type);
+    if (own != caller) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), caller);
+    return t;
   }
 };
 
