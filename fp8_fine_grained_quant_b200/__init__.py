@@ -6,6 +6,12 @@ kernels behind the C ABI declared in ``include/fp8q.h``; PyTorch provides the
 device memory and the stream.  There is no CPU fallback: if the library is
 missing or the device is not sm_100, the calls raise.
 
+Every call runs on the device's current stream, or on the one that ``stream`` (a
+``torch.cuda.Stream`` or a handle) names.  The arguments of a call on another
+stream must be ready there, and stay as they are until it has run; what it
+allocates belongs to that stream, which the current one waits for before it uses
+an output.
+
 Names and semantics match the C entry points:
 
 * :func:`fp8_quant_act_1x128`  -- bf16 [M,K] -> E4M3 [M,K] + f32 scales [M,K/128]
@@ -198,6 +204,24 @@ _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 
 
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream`.  Where that is not the current stream the memory comes from its own pool (a
+    block of the current stream's pool may have work of that stream queued on it), and is handed out again only
+    after the work that the current stream had queued on it when it was dropped."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    handle = _stream(stream, device)
+    handle = 0 if handle == 1 else handle  # cudaStreamLegacy is the default stream
+    if handle == here.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    other = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(other):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 def _p(t):
     return None if t is None else t.data_ptr()  # ctypes makes the pointer (argtypes)
 
@@ -219,9 +243,9 @@ def fp8_quant_act_1x128(x: torch.Tensor, q: torch.Tensor | None = None, s: torch
     _numel(s, M * (K // TILE), "s")
     dev = _device_of(x=x, q=q, s=s)
     if q is None:
-        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+        q = _empty((M, K), torch.float8_e4m3fn, dev, stream)
     if s is None:
-        s = torch.empty((M, K // TILE), dtype=torch.float32, device=dev)
+        s = _empty((M, K // TILE), torch.float32, dev, stream)
     with _on(dev):
         _check(getattr(lib(), _entry)(_p(x), M, K, _p(q), _p(s), _stream(stream, dev)), _entry)
     return q, s
@@ -241,9 +265,9 @@ def fp8_quant_w_128x128(w: torch.Tensor, q: torch.Tensor | None = None, s: torch
     _numel(s, G * (N // TILE) * (K // TILE), "s")
     dev = _device_of(w=w, q=q, s=s)
     if q is None:
-        q = torch.empty(tuple(w.shape), dtype=torch.float8_e4m3fn, device=dev)
+        q = _empty(tuple(w.shape), torch.float8_e4m3fn, dev, stream)
     if s is None:
-        s = torch.empty(lead + (N // TILE, K // TILE), dtype=torch.float32, device=dev)
+        s = _empty(lead + (N // TILE, K // TILE), torch.float32, dev, stream)
     with _on(dev):
         _check(getattr(lib(), _entry)(_p(w), G, N, K, _p(q), _p(s), _stream(stream, dev)), _entry)
     return q, s
@@ -268,13 +292,13 @@ def fp8_quant_act_w(x: torch.Tensor, w: torch.Tensor, qa: torch.Tensor | None = 
     _numel(sw, G * (N // TILE) * (Kw // TILE), "sw")
     dev = _device_of(x=x, w=w, qa=qa, sa=sa, qw=qw, sw=sw)
     if qa is None:
-        qa = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+        qa = _empty((M, K), torch.float8_e4m3fn, dev, stream)
     if sa is None:
-        sa = torch.empty((M, K // TILE), dtype=torch.float32, device=dev)
+        sa = _empty((M, K // TILE), torch.float32, dev, stream)
     if qw is None:
-        qw = torch.empty(tuple(w.shape), dtype=torch.float8_e4m3fn, device=dev)
+        qw = _empty(tuple(w.shape), torch.float8_e4m3fn, dev, stream)
     if sw is None:
-        sw = torch.empty(tuple(w.shape[:-2]) + (N // TILE, Kw // TILE), dtype=torch.float32, device=dev)
+        sw = _empty(tuple(w.shape[:-2]) + (N // TILE, Kw // TILE), torch.float32, dev, stream)
     with _on(dev):
         _check(lib().fp8_quant_act_w(_p(x), M, K, _p(qa), _p(sa), _p(w), G, N, Kw, _p(qw), _p(sw),
                                      _stream(stream, dev)), "fp8_quant_act_w")
@@ -303,9 +327,9 @@ def fp8_quant_act_128x1(x: torch.Tensor, q: torch.Tensor | None = None, s: torch
     _numel(s, nmb * K, "s")
     dev = _device_of(x=x, q=q, s=s)
     if q is None:
-        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+        q = _empty((M, K), torch.float8_e4m3fn, dev, stream)
     if s is None:
-        s = torch.empty((nmb, K), dtype=torch.float32, device=dev)
+        s = _empty((nmb, K), torch.float32, dev, stream)
     with _on(dev):
         _check(lib().fp8_quant_act_128x1(_p(x), M, K, _p(q), _p(s), _stream(stream, dev)), "fp8_quant_act_128x1")
     return q, s
@@ -333,9 +357,9 @@ def fp8_quant_act_128x1_t(x: torch.Tensor, qt: torch.Tensor | None = None, s: to
     _numel(s, (Mp // TILE) * K, "s")
     dev = _device_of(x=x, qt=qt, s=s)
     if qt is None:
-        qt = torch.empty((K, Mp), dtype=torch.float8_e4m3fn, device=dev)
+        qt = _empty((K, Mp), torch.float8_e4m3fn, dev, stream)
     if s is None:
-        s = torch.empty((Mp // TILE, K), dtype=torch.float32, device=dev)
+        s = _empty((Mp // TILE, K), torch.float32, dev, stream)
     with _on(dev):
         _check(lib().fp8_quant_act_128x1_t(_p(x), M, K, Mp, _p(qt), _p(s), _stream(stream, dev)),
                "fp8_quant_act_128x1_t")
@@ -359,9 +383,9 @@ def fp8_transpose_w_128x128(q: torch.Tensor, s: torch.Tensor, qt: torch.Tensor |
     _numel(st, G * (N // TILE) * (K // TILE), "st")
     dev = _device_of(q=q, s=s, qt=qt, st=st)
     if qt is None:
-        qt = torch.empty(lead + (K, N), dtype=torch.float8_e4m3fn, device=dev)
+        qt = _empty(lead + (K, N), torch.float8_e4m3fn, dev, stream)
     if st is None:
-        st = torch.empty(lead + (K // TILE, N // TILE), dtype=torch.float32, device=dev)
+        st = _empty(lead + (K // TILE, N // TILE), torch.float32, dev, stream)
     with _on(dev):
         _check(lib().fp8_transpose_w_128x128(_p(q), _p(s), G, N, K, _p(qt), _p(st), _stream(stream, dev)),
                "fp8_transpose_w_128x128")
@@ -394,9 +418,9 @@ def fp8_swiglu_quant_1x128(c1: torch.Tensor, masked_m: torch.Tensor | None = Non
     _numel(sh, rows * (inter // TILE), "sh")
     dev = _device_of(c1=c1, masked_m=masked_m, qh=qh, sh=sh)
     if qh is None:
-        qh = torch.empty(lead + (inter,), dtype=torch.float8_e4m3fn, device=dev)
+        qh = _empty(lead + (inter,), torch.float8_e4m3fn, dev, stream)
     if sh is None:
-        sh = torch.empty(lead + (inter // TILE,), dtype=torch.float32, device=dev)
+        sh = _empty(lead + (inter // TILE,), torch.float32, dev, stream)
     with _on(dev):
         _check(lib().fp8_swiglu_quant_1x128(_p(c1), rows, inter, _p(masked_m), cap, _p(qh), _p(sh),
                                             _stream(stream, dev)), "fp8_swiglu_quant_1x128")
@@ -426,7 +450,7 @@ def fp8_gemm_blockscaled(qa, sa, qb, sb, out: torch.Tensor | None = None, stream
     """C[M,N] (bf16) = A * B^T from 1x128-quantized A and 128x128-quantized B."""
     M, N, K, dev = _dense_operands(qa, sa, qb, sb, out)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        out = _empty((M, N), torch.bfloat16, dev, stream)
     with _on(dev):
         _check(lib().fp8_gemm_blockscaled(_p(qa), _p(sa), _p(qb), _p(sb), _p(out), M, N, K,
                                           _stream(stream, dev)), "fp8_gemm_blockscaled")
@@ -437,7 +461,7 @@ def fp8_gemm_unpromoted_diag(qa, sa, qb, sb, out: torch.Tensor | None = None, st
     """Diagnostic: all of K accumulated in the tensor cores, scaled once (per-tensor scales only)."""
     M, N, K, dev = _dense_operands(qa, sa, qb, sb, out)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        out = _empty((M, N), torch.bfloat16, dev, stream)
     with _on(dev):
         _check(lib().fp8_gemm_unpromoted_diag(_p(qa), _p(sa), _p(qb), _p(sb), _p(out), M, N, K,
                                               _stream(stream, dev)), "fp8_gemm_unpromoted_diag")
@@ -466,7 +490,7 @@ def fp8_gemm_wgrad(q_dy_t, s_dy, q_x_t, s_x, out: torch.Tensor | None = None, st
     _numel(out, N * K, "out")
     dev = _device_of(q_dy_t=q_dy_t, s_dy=s_dy, q_x_t=q_x_t, s_x=s_x, out=out)
     if out is None:
-        out = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+        out = _empty((N, K), torch.bfloat16, dev, stream)
     with _on(dev):
         _check(lib().fp8_gemm_wgrad(_p(q_dy_t), _p(s_dy), _p(q_x_t), _p(s_x), _p(out), N, K, Mp,
                                     _stream(stream, dev)), "fp8_gemm_wgrad")
@@ -485,7 +509,7 @@ def fp8_mx_scales_act(sa: torch.Tensor, out: torch.Tensor | None = None, stream=
     _numel(out, mt * nkb * MX_ATOM, "out")
     dev = _device_of(sa=sa, out=out)
     if out is None:
-        out = torch.empty((mt, nkb, MX_ATOM), dtype=torch.uint8, device=dev)
+        out = _empty((mt, nkb, MX_ATOM), torch.uint8, dev, stream)
     with _on(dev):
         _check(lib().fp8_mx_scales_act(_p(sa), M, nkb * TILE, _p(out), _stream(stream, dev)), "fp8_mx_scales_act")
     return out
@@ -499,7 +523,7 @@ def fp8_mx_scales_w(sb: torch.Tensor, out: torch.Tensor | None = None, stream=No
     _numel(out, G * nnb * nkb * MX_ATOM, "out")
     dev = _device_of(sb=sb, out=out)
     if out is None:
-        out = torch.empty((G * nnb, nkb, MX_ATOM), dtype=torch.uint8, device=dev)
+        out = _empty((G * nnb, nkb, MX_ATOM), torch.uint8, dev, stream)
     with _on(dev):
         _check(lib().fp8_mx_scales_w(_p(sb), G, nnb * TILE, nkb * TILE, _p(out), _stream(stream, dev)),
                "fp8_mx_scales_w")
@@ -525,7 +549,7 @@ def fp8_gemm_mx(qa, sfa_mx, qb, sfb_mx, out: torch.Tensor | None = None, stream=
     _numel(out, M * N, "out")
     dev = _device_of(qa=qa, sfa_mx=sfa_mx, qb=qb, sfb_mx=sfb_mx, out=out)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        out = _empty((M, N), torch.bfloat16, dev, stream)
     with _on(dev):
         _check(lib().fp8_gemm_mx(_p(qa), _p(sfa_mx), _p(qb), _p(sfb_mx), _p(out), M, N, K, _stream(stream, dev)),
                "fp8_gemm_mx")
@@ -554,7 +578,7 @@ def fp8_grouped_gemm_mx_contiguous(qa, sfa_mx, qb, sfb_mx, m_indices, out: torch
     _numel(out, M_tot * N, "out")
     dev = _device_of(qa=qa, sfa_mx=sfa_mx, qb=qb, sfb_mx=sfb_mx, m_indices=m_indices, out=out)
     if out is None:
-        out = torch.empty((M_tot, N), dtype=torch.bfloat16, device=dev)
+        out = _empty((M_tot, N), torch.bfloat16, dev, stream)
     with _on(dev):
         _check(lib().fp8_grouped_gemm_mx_contiguous(_p(qa), _p(sfa_mx), _p(qb), _p(sfb_mx), _p(m_indices), _p(out),
                                                     M_tot, N, K, E, _stream(stream, dev)),
@@ -584,7 +608,7 @@ def fp8_grouped_gemm_mx_masked(qa, sfa_mx, qb, sfb_mx, masked_m, out: torch.Tens
     _numel(out, E * cap * N, "out")
     dev = _device_of(qa=qa, sfa_mx=sfa_mx, qb=qb, sfb_mx=sfb_mx, masked_m=masked_m, out=out)
     if out is None:
-        out = torch.empty((E, cap, N), dtype=torch.bfloat16, device=dev)
+        out = _empty((E, cap, N), torch.bfloat16, dev, stream)
     with _on(dev):
         _check(lib().fp8_grouped_gemm_mx_masked(_p(qa), _p(sfa_mx), _p(qb), _p(sfb_mx), _p(masked_m), _p(out), E,
                                                 cap, N, K, _stream(stream, dev)), "fp8_grouped_gemm_mx_masked")
@@ -614,7 +638,7 @@ def fp8_grouped_gemm_contiguous(qa, sa, qb, sb, m_indices, out: torch.Tensor | N
     _numel(out, M_tot * N, "out")
     dev = _device_of(qa=qa, sa=sa, qb=qb, sb=sb, m_indices=m_indices, out=out)
     if out is None:
-        out = torch.empty((M_tot, N), dtype=torch.bfloat16, device=dev)
+        out = _empty((M_tot, N), torch.bfloat16, dev, stream)
     with _on(dev):
         _check(lib().fp8_grouped_gemm_contiguous(_p(qa), _p(sa), _p(qb), _p(sb), _p(m_indices), _p(out), M_tot, N, K,
                                                  E, _stream(stream, dev)), "fp8_grouped_gemm_contiguous")
@@ -645,7 +669,7 @@ def fp8_grouped_gemm_masked(qa, sa, qb, sb, masked_m, expected_m: int = 0, out: 
     _numel(out, E * cap * N, "out")
     dev = _device_of(qa=qa, sa=sa, qb=qb, sb=sb, masked_m=masked_m, out=out)
     if out is None:
-        out = torch.empty((E, cap, N), dtype=torch.bfloat16, device=dev)
+        out = _empty((E, cap, N), torch.bfloat16, dev, stream)
     with _on(dev):
         _check(lib().fp8_grouped_gemm_masked(_p(qa), _p(sa), _p(qb), _p(sb), _p(masked_m), _p(out), E, cap, N, K,
                                              int(expected_m), _stream(stream, dev)), "fp8_grouped_gemm_masked")

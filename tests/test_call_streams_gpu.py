@@ -221,3 +221,83 @@ def test_named_stream_inside_a_captured_graph(dev, side):
         assert all(bool((t == 7).all()) for t in junk)
         for ref, out in ((moe.layout_contiguous(host, E), a), (moe.layout_masked(host, E, 1024), b)):
             assert all(np.array_equal(x, y.cpu().numpy()) for x, y in zip(ref, out))
+
+
+def _gemm_and_quantizer_calls(dev):
+    """name -> call(stream): the calls marshalled in Python, with fresh outputs."""
+    g = torch.Generator(device=dev).manual_seed(4)
+
+    def bf16(*shape):
+        return torch.randn(shape, generator=g, device=dev).bfloat16()
+
+    x, w, wg, c1 = bf16(256, 512), bf16(128, 512), bf16(2, 128, 512), bf16(256, 512)
+    qa, sa = fq.fp8_quant_act_1x128(x)
+    qw, sw = fq.fp8_quant_w_128x128(w)
+    qg, sg = fq.fp8_quant_w_128x128(wg)
+    pa, ta = fq.fp8_quant_act_1x128_ue8m0(x)
+    pw, tw = fq.fp8_quant_w_128x128_ue8m0(w)
+    pg, tg = fq.fp8_quant_w_128x128_ue8m0(wg)
+    xt, st = fq.fp8_quant_act_128x1_t(x)
+    ma, mw, mg = fq.fp8_mx_scales_act(ta), fq.fp8_mx_scales_w(tw), fq.fp8_mx_scales_w(tg)
+    ta3 = ta.view(2, 128, 4)
+    ma3 = torch.cat([fq.fp8_mx_scales_act(ta3[e]) for e in range(2)])
+    m_indices = torch.tensor([1, 0], dtype=torch.int32, device=dev)
+    masked_m = torch.tensor([128, 128], dtype=torch.int32, device=dev)
+    qa3, sa3, pa3 = qa.view(2, 128, 512), sa.view(2, 128, 4), pa.view(2, 128, 512)
+    torch.cuda.synchronize(dev)
+    return {
+        "quant_act": lambda s: fq.fp8_quant_act_1x128(x, stream=s),
+        "quant_w": lambda s: fq.fp8_quant_w_128x128(w, stream=s),
+        "quant_act_w": lambda s: [t for p in fq.fp8_quant_act_w(x, w, stream=s) for t in p],
+        "quant_act_ue8m0": lambda s: fq.fp8_quant_act_1x128_ue8m0(x, stream=s),
+        "quant_w_ue8m0": lambda s: fq.fp8_quant_w_128x128_ue8m0(w, stream=s),
+        "quant_act_128x1": lambda s: fq.fp8_quant_act_128x1(x, stream=s),
+        "quant_act_128x1_t": lambda s: fq.fp8_quant_act_128x1_t(x, stream=s),
+        "transpose": lambda s: fq.fp8_transpose_w_128x128(qw, sw, stream=s),
+        "swiglu": lambda s: fq.fp8_swiglu_quant_1x128(c1, stream=s),
+        "gemm": lambda s: [fq.fp8_gemm_blockscaled(qa, sa, qw, sw, stream=s)],
+        "gemm_unpromoted": lambda s: [fq.fp8_gemm_unpromoted_diag(qa, sa, qw, sw, stream=s)],
+        "wgrad": lambda s: [fq.fp8_gemm_wgrad(xt, st, xt, st, stream=s)],
+        "grouped": lambda s: [fq.fp8_grouped_gemm_contiguous(qa, sa, qg, sg, m_indices, stream=s)],
+        "masked": lambda s: [fq.fp8_grouped_gemm_masked(qa3, sa3, qg, sg, masked_m, stream=s)],
+        "mx_scales_act": lambda s: [fq.fp8_mx_scales_act(ta, stream=s)],
+        "mx_scales_w": lambda s: [fq.fp8_mx_scales_w(tw, stream=s)],
+        "gemm_mx": lambda s: [fq.fp8_gemm_mx(pa, ma, pw, mw, stream=s)],
+        "grouped_mx": lambda s: [fq.fp8_grouped_gemm_mx_contiguous(pa, ma, pg, mg, m_indices, stream=s)],
+        "masked_mx": lambda s: [fq.fp8_grouped_gemm_mx_masked(pa3, ma3, pg, mg, masked_m, stream=s)],
+    }
+
+
+@pytest.mark.parametrize("how", ["stream", "handle"])
+def test_outputs_of_gemms_and_quantizers_belong_to_the_named_stream(dev, side, how):
+    for name, call in _gemm_and_quantizer_calls(dev).items():
+        mine = call(None)
+        torch.cuda.synchronize(dev)
+        theirs = call(side if how == "stream" else side.cuda_stream)
+        torch.cuda.synchronize(dev)
+        for a, b in zip(mine, theirs):
+            assert _stream_of(a) == 0, name
+            assert _stream_of(b) == side.cuda_stream, name
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
+    assert fq.get_device_error(device=dev) == fq.OK
+
+
+def test_gemms_and_quantizers_on_the_current_stream_by_name(dev, side):
+    calls = _gemm_and_quantizer_calls(dev)
+    for stream in (0, 1, torch.cuda.default_stream(dev)):
+        for name, call in calls.items():
+            assert all(_stream_of(t) == 0 for t in call(stream)), name
+    with torch.cuda.stream(side):
+        for name, call in calls.items():
+            assert all(_stream_of(t) == side.cuda_stream for t in call(side)), name
+            assert all(_stream_of(t) == 0 for t in call(0)), name
+            assert all(_stream_of(t) == 0 for t in call(1)), name
+    torch.cuda.synchronize(dev)
+    assert fq.get_device_error(device=dev) == fq.OK
+
+
+def test_quantizers_leave_memory_of_other_streams_alone(dev, side):
+    x1, x2 = (torch.randn((4096, 1024), device=dev).bfloat16() for _ in range(2))
+    _freed_block_is_left_alone(dev, lambda s: fq.fp8_quant_act_1x128(x1, stream=s))
+    _output_outlives_queued_work(dev, side, lambda s: fq.fp8_quant_act_1x128(x1, stream=s),
+                                 lambda s: fq.fp8_quant_act_1x128(x2, stream=s))
