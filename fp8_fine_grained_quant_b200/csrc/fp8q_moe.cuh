@@ -1036,17 +1036,28 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(LayoutArgs a
 
 // ---------------------------------------------------------------------------
 // Rows of the contiguous layout that no entry fills: in the last block of each
-// expert, the rows past its count.  Row r is one when its block has an expert,
-// the next block another one, and r lies past the count's remainder.
+// expert, the rows past its count.  Where the next block has another expert, the
+// block is its expert's last.  The last block of the buffer may end before its
+// expert's run does (fewer rows than the layout needs: the slots beyond are
+// skipped), so there the block's place in the run, which starts at the first block
+// with an index of e or more, says which entries it holds.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ bool is_pad_row(int64_t row, const int32_t* m_indices, const int32_t* counts, int E,
                                            int64_t blocks) {
   const int64_t b = row >> 7;
   const int e = m_indices[b];
   if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(E)) return false;
-  if (b + 1 < blocks && m_indices[b + 1] == e) return false;
-  const int rest = counts[e] & 127;
-  return rest != 0 && static_cast<int>(row & 127) >= rest;
+  if (b + 1 < blocks) {
+    if (m_indices[b + 1] == e) return false;
+    const int rest = counts[e] & 127;
+    return rest != 0 && static_cast<int>(row & 127) >= rest;
+  }
+  int64_t lo = 0, hi = b;  // the run's first block lies in [lo, hi]
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (m_indices[mid] < e) lo = mid + 1; else hi = mid;
+  }
+  return (b - lo) * 128 + (row & 127) >= counts[e];
 }
 
 // ---------------------------------------------------------------------------

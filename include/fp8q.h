@@ -381,7 +381,8 @@ FP8Q_API int64_t fp8_moe_layout_workspace(int64_t T, int64_t top_k, int64_t E);
  *   q : [rows, D] E4M3, s : [rows, D/128] f32, written where a slot points.
  *   m_indices [rows/128], counts [E] : both NULL, or the contiguous layout's;
  *            then the rows that pad an expert's last block get codes 0 and
- *            scale 1 (rows a multiple of 128).
+ *            scale 1 (rows a multiple of 128; fewer than the layout's cut it off
+ *            at any block, rows past the cut are skipped).
  * Other rows (past masked_m, blocks past the last) are left as they were.
  * D a multiple of 128, T * D / 128 below 2^31.  x 32-byte, q 16-byte, the
  * others 4-byte aligned.
