@@ -1026,8 +1026,9 @@ int fp8_moe_combine_bwd(const void* dout_bf16, const void* y_bf16, int64_t rows,
   if (bad_tokens(T, top_k, D, rows)) return FP8Q_ERR_SHAPE;
   int rc = check_layout(m_indices, counts, E, rows);
   if (rc) return rc;
-  if (T == 0 || D == 0) return FP8Q_OK;
-  if (!dout_bf16 || (rows && (!y_bf16 || !dy_bf16)) || !slots || !weights || !dweights) return FP8Q_ERR_NULL;
+  if (T == 0) return FP8Q_OK;
+  // no channels: no rows to read or write, but dweights are sums of none
+  if ((D && (!dout_bf16 || (rows && (!y_bf16 || !dy_bf16)))) || !slots || !weights || !dweights) return FP8Q_ERR_NULL;
   if (!aligned(dout_bf16, 16) || !aligned(y_bf16, 16) || !aligned(dy_bf16, 16) || !aligned(slots, 4) ||
       !aligned(weights, 4) || !aligned(dweights, 4))
     return FP8Q_ERR_ALIGN;
