@@ -78,6 +78,14 @@ void multiple(int64_t v, const char* name) {
   if (v % kTile) bad_value(name, " = ", v, " is not a multiple of ", kTile);
 }
 
+// An output may not share memory with an input whose elements other threads still read.
+void apart(const Opt& out, const char* name, const Tensor& in, const char* other, const char* why) {
+  if (!out || out->numel() == 0 || in.numel() == 0) return;
+  const auto a = reinterpret_cast<uintptr_t>(out->data_ptr()), b = reinterpret_cast<uintptr_t>(in.data_ptr());
+  if (a < b + in.nbytes() && b < a + out->nbytes())
+    bad_value(name, " may not be ", other, ", or overlap it: ", why);
+}
+
 // All tensors are CUDA tensors on one device (there is no CPU path).
 struct Place {
   std::optional<at::Device> dev;
@@ -330,6 +338,7 @@ Tensor combine(const Tensor& y, const Tensor& slots, const Opt& weights, const O
   p.add(slots, "slots");
   p.add(weights, "weights");
   p.add(out, "out");
+  apart(out, "out", y, "y", "its rows are read while out is written");
   const On on(p, stream);
   const Tensor o = on.fresh(out, {T, D}, at::kBFloat16);
   check(fp8_moe_combine(ptr(y), rows, D, ptr<int32_t>(slots), ptr<float>(weights), T, top_k, ptr(o), on.stream),
@@ -360,8 +369,8 @@ py::tuple combine_bwd(const Tensor& dout, const Tensor& y, const Tensor& slots, 
   p.add(counts, "counts");
   p.add(dy, "dy");
   p.add(dweights, "dweights");
-  if (dy && dy->numel() && dy->data_ptr() == y.data_ptr())
-    bad_value("dy may not be y: its rows are read while dy is written");
+  apart(dy, "dy", y, "y", "its rows are read while dy is written");
+  apart(dy, "dy", dout, "dout", "its rows are read while dy is written");
   const On on(p, stream);
   const Tensor od = on.fresh(dy, y.sizes(), at::kBFloat16), ow = on.fresh(dweights, {T, top_k}, at::kFloat);
   check(fp8_moe_combine_bwd(ptr(dout), ptr(y), rows, D, ptr<int32_t>(slots), ptr<float>(weights), T, top_k,
@@ -415,10 +424,9 @@ py::tuple swiglu_bwd(const Tensor& dh, const Tensor& qc, const Tensor& sc, const
   p.add(dc, "dc");
   p.add(q, "q");
   p.add(s, "s");
-  if (q && q->numel() && q->data_ptr() == qc.data_ptr())
-    bad_value("q may not be qc: the checkpoint is read while q is written");
-  if (s && s->numel() && s->data_ptr() == sc.data_ptr())
-    bad_value("s may not be sc: the checkpoint is read while s is written");
+  apart(q, "q", qc, "qc", "the checkpoint is read while q is written");
+  apart(s, "s", sc, "sc", "the checkpoint is read while s is written");
+  apart(dc, "dc", dh, "dh", "it is read while dc is written");
   const On on(p, stream);
   const Tensor a = on.fresh(dc, {rows, 2 * inter}, at::kBFloat16),
                b = on.fresh(q, {rows, 2 * inter}, at::kFloat8_e4m3fn), c = on.fresh(s, {rows, 2 * nt}, at::kFloat);

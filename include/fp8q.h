@@ -397,7 +397,8 @@ FP8Q_API int fp8_moe_dispatch_1x128(const void* x_bf16, int64_t T, int64_t D, co
  * sum: the gradient of the dispatch with respect to its tokens.  Entries whose
  * slot lies outside [0, rows) count for nothing (their y is not read); a token
  * with none gets zeros.
- *   y_bf16 : [rows, D] bf16.  out_bf16 : [T, D] bf16, every element written.
+ *   y_bf16 : [rows, D] bf16.  out_bf16 : [T, D] bf16, every element written; it
+ *            may not overlap y.
  * Sizes as above; y and out 16-byte, slots and weights 4-byte aligned.
  */
 FP8Q_API int fp8_moe_combine(const void* y_bf16, int64_t rows, int64_t D, const int32_t* slots, const float* weights,
@@ -410,7 +411,7 @@ FP8Q_API int fp8_moe_combine(const void* y_bf16, int64_t rows, int64_t D, const 
  *              rows get zeros; other rows are left as they were.
  *   dweights : [T, top_k] f32: <dout[t], y[slots[t, j]]>, 0 without a slot.
  *   dout_bf16 : [T, D] bf16.  weights : [T, top_k] f32 (required).
- * The valid slots are distinct.  dy may not overlap y.
+ * The valid slots are distinct.  dy may not overlap y or dout.
  */
 FP8Q_API int fp8_moe_combine_bwd(const void* dout_bf16, const void* y_bf16, int64_t rows, int64_t D,
                                  const int32_t* slots, const float* weights, int64_t T, int64_t top_k,
@@ -441,7 +442,8 @@ FP8Q_API int fp8_swiglu_ckpt_1x128(const void* c1_bf16, int64_t rows, int64_t in
  *   q, s    : [rows, 2*inter] E4M3, [rows, 2*inter/128] f32, written: the 1x128
  *             quantization of the FP32 values d (not of their bf16 rounding),
  *             the operand of the activation gradient's GEMM.
- * Sizes as above; dh 32-byte, dc, qc and q 16-byte, sc and s 4-byte aligned.
+ * No output may overlap an input.  Sizes as above; dh 32-byte, dc, qc and q
+ * 16-byte, sc and s 4-byte aligned.
  */
 FP8Q_API int fp8_swiglu_bwd_1x128(const void* dh_bf16, const uint8_t* qc, const float* sc, int64_t rows, int64_t inter,
                                   void* dc_bf16, uint8_t* q, float* s, cudaStream_t stream);
