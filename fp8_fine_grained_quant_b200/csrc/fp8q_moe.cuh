@@ -769,6 +769,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_bwd_kernel(RouteBw
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       x[i] = x[i] > neg_inf_f32() ? expf(x[i] - m) : 0.0f;
+      o[i] = x[i] > 0.0f ? o[i] : 0.0f;  // not 0 times a gradient of inf or NaN
       sum += x[i];
       dot = fmaf(x[i], o[i], dot);
     }
