@@ -491,7 +491,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 8 ? kRouteCtasPerSm :
         // each total's least and largest possible value: it is off by as much as its keys are, and they may cancel
         const float err = tol + 0x1p-20f * mag;
         const float w = redux_min(keep ? fmaxf(total - err, neg_inf_f32()) : __int_as_float(0x7F800000));
-        const float b = redux_max(in && !keep ? fmaxf(total + err, neg_inf_f32()) : neg_inf_f32());  // NaN: no key
+        // (-inf only for a group without a key: a sum below FP32's range is one of the least finite ones)
+        const float least = b1 > neg_inf_f32() ? -FLT_MAX : neg_inf_f32();
+        const float b = redux_max(in && !keep ? fmaxf(total + err, least) : neg_inf_f32());
         if (!(b == neg_inf_f32() || w > b)) {
           if constexpr (VPL <= kExactVpl) {
             // the groups' sums in binary64, of the keys that can be among their best: each lane's

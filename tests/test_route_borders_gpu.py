@@ -127,3 +127,22 @@ def test_group_sums_of_very_large_and_infinite_biases(dev, score):
     bias[4 * size:4 * size + 2] = -3.4e38
     for KG in (1, 2, 3, 4, 5, 7, 8):
         _same_ids(dev, l, 2, bias=bias, score=score, n_group=G, topk_group=KG, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(64, 8), (60, 15), (512, 8), (1024, 8)])
+def test_group_sums_below_the_range_come_before_groups_without_experts(dev, score, E, G):
+    """Two biases of -3.4e38 make a sum that only binary64 holds; a group whose
+    experts are all masked has none."""
+    rng = np.random.default_rng(E)
+    size = E // G
+    for low in (-3.4e38, -2e38):
+        l = rng.standard_normal((30, E)).astype(np.float32)
+        bias = np.full(E, low, np.float32)
+        l[:, np.arange(E) % size > 2] = -np.inf                 # three experts a group
+        bias[2 * size:3 * size] = 0.1
+        l[:, :size] = -np.inf                                   # the first group is empty
+        bias[size + 1:2 * size] = -np.inf                       # one expert left in the second
+        l[::3, (G - 1) * size:] = -np.inf                       # the last is empty too
+        for KG in range(1, G + 1):
+            _same_ids(dev, l, min(KG * size, 3 * G, 32), bias=bias, score=score, n_group=G, topk_group=KG, group_top=2)
