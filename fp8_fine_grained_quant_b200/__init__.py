@@ -738,7 +738,8 @@ def fp8_moe_dispatch_1x128(x: torch.Tensor, slots: torch.Tensor, rows: int, m_in
                            s: torch.Tensor | None = None, stream=None):
     """Tokens x [T,D] bf16, 1x128-quantized once each, into the rows of their slots [T,k]: returns (q [rows,D]
     float8_e4m3fn, s [rows,D/128] f32).  With the contiguous layout's m_indices and counts, the rows that pad an
-    expert's last block get codes 0 and scale 1.  Other rows are left as they were: pass q and s to keep them."""
+    expert's last block get codes 0 and scale 1.  Other rows are left as they were: pass q and s to keep them.  The
+    slots in [0, rows) are distinct, as the layouts give them; others are skipped."""
     return _native().dispatch_1x128(x, slots, rows, m_indices, counts, q, s, stream)
 
 
@@ -754,7 +755,8 @@ def fp8_moe_combine_bwd(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tensor
                         dy: torch.Tensor | None = None, dweights: torch.Tensor | None = None, stream=None):
     """Gradient of :func:`fp8_moe_combine`: dout [T,D] bf16 -> (dy, the shape of y, bf16; dweights [T,k] f32).
     Row slots[t,j] of dy gets weights[t,j] * dout[t]; with the contiguous layout's m_indices and counts the pad
-    rows get zeros; other rows are left as they were: pass dy to keep them."""
+    rows get zeros; other rows are left as they were: pass dy (not over y or dout) to keep them.  The slots in
+    [0, rows) are distinct."""
     return _native().combine_bwd(dout, y, slots, weights, m_indices, counts, dy, dweights, stream)
 
 

@@ -60,7 +60,10 @@ __device__ __forceinline__ void e4m3x4_to_f32x2(uint32_t c, uint64_t& p0, uint64
 
 // ------------------------------------------------------------ codes by a corrected quotient
 // The code of fl32(x / s) without a division, a bracket or a branch: with
-// y = RN(1/s), q0 = x y, q1 = q0 + (x - q0 s) y.  Away from the E4M3 midpoints
+// y = RN(1/s), q0 = x y, q1 = q0 + (x - q0 s) y, the remainder step of P. W.
+// Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", IBM J. Res. Dev. 34 (1990).  What follows is only that the code is
+// right, which needs less than the quotient's own last bit.  Away from the E4M3 midpoints
 // q1 and fl32(x / s) are on the same side of each.  They could part only where
 // x / s is next to an FP32 rounding midpoint beside an E4M3 midpoint; there q0
 // is one of the two floats around it (x y is off by less than an ulp), x - q0 s

@@ -379,8 +379,10 @@ constexpr int kRouteCtasPerSm = 8;  // up to eight experts a lane: 64 registers
 //
 // Bound by instruction issue (about 790 a row of 256 experts, half of them on the
 // integer and compare pipe), not by its bytes: 32768 rows of 256 experts in 8
-// groups, biased sigmoid, take 36.7 us on a B200 against 5.5 us for reading them;
-// 4096 rows of 32 take 3.1 us and one row 3.1 us, a launch's time.  (All keys in
+// groups, biased sigmoid, take 37.0 us on a B200 against 5.5 us for reading them;
+// 4096 rows of 32 take 3.1 us and one row 3.1 us, a launch's time.  Rows of nothing
+// but equal keys, which border_is_equal reads again, take 46 us for 32768 of 256
+// without groups, 117 where the groups are equal too.  (All keys in
 // binary64: 121 us; a row that left its choice to route_choose_f64 alone held up
 // the launch's end by 7 us.)  The errors, by exp_approx's:
 //   sigmoid  p (1 - p) (2 + |x|) 2^-23 <= 2^-23, + 2^-24 from 1 + e and 2^-23

@@ -140,7 +140,8 @@ def test_layouts_on_two_streams_behind_other_work(dev, side):
     for _ in range(3):
         hold.append(_busy(dev, 5))
         for _ in range(4):
-            got.append([fq.fp8_moe_layout_contiguous(devs[0], 64), fq.fp8_moe_layout_contiguous(devs[1], 64, stream=side)])
+            got.append([fq.fp8_moe_layout_contiguous(devs[0], 64),
+                        fq.fp8_moe_layout_contiguous(devs[1], 64, stream=side)])
     torch.cuda.synchronize(dev)
     refs = [moe.layout_contiguous(h, 64) for h in hosts]
     for pair in got:

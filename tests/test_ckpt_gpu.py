@@ -2,10 +2,13 @@
 from there, the weight-gradient operand, and a training step of the expert MLP
 made of them.
 
-Bounds (u = 2^-24): with expf and div.full within 2 ulp (4u) and the rounded
-adds and products, p is off by at most 12u relative and 1 - p = e p by 20u; the
-magnitudes that the oracle returns (|dh u| p (|g| (1 - p) + |1 + g (1 - p)|) and
-|dh g p|) times 32u = 2^-19 bound d; its bf16 rounding adds 2^-8.
+Bounds (u = 2^-24): exp(-|g|) is the square of an ex2.approx (4u, so 8u, and 0.6u
+of roundings), rcp.approx is within 2u, sums and products within 1u each.  Of p and
+1 - p the larger, r = 1 / (1 + e), is off by at most 4.3u + 3u = 7.3u relative, the
+smaller, e r, by 8.6u + 4u = 12.6u (an error of e reaches them as e / (1 + e) and
+1 / (1 + e) of it).  With three products and the sum 1 + g (1 - p), d is within 17u
+of the magnitudes that the oracle returns (|dh u| p (|g| (1 - p) + |1 + g (1 - p)|)
+and |dh g p|); the tests allow 32u = 2^-19, and 2^-8 for the bf16 rounding.
 """
 import numpy as np
 import pytest

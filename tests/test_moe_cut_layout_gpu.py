@@ -45,7 +45,8 @@ def test_dispatch_into_a_cut_layout(dev, blocks):
     x = _bf16(rng, (sum(COUNTS), D))
     q = torch.full((rows, D), 0x5A, dtype=torch.uint8, device=dev)
     s = torch.full((rows, D // 128), -3.0, device=dev)
-    fq.fp8_moe_dispatch_1x128(to_torch_bf16(x, dev), slots, rows, m_indices=m[:blocks].contiguous(), counts=counts, q=q, s=s)
+    fq.fp8_moe_dispatch_1x128(to_torch_bf16(x, dev), slots, rows, m_indices=m[:blocks].contiguous(), counts=counts,
+                              q=q, s=s)
     oq, os_ = oracle.quant_act_1x128(x)
     eq, es = np.full((rows, D), 0x5A, np.uint8), np.full((rows, D // 128), -3.0, np.float32)
     pad = moe.pad_rows(om, oc)[:rows]
