@@ -377,7 +377,7 @@ constexpr int kRouteCtasPerSm = 8;  // up to eight experts a lane: 64 registers
 // the chosen and those next to the last of them.  Shares above eight experts, and
 // more than 32 keys in reach, take route_choose_f64.
 //
-// Bound by instruction issue (about 790 a row of 256 experts, half of them on the
+// Bound by instruction issue (about 810 a row of 256 experts, half of them on the
 // integer and compare pipe), not by its bytes: 32768 rows of 256 experts in 8
 // groups, biased sigmoid, take 37.0 us on a B200 against 5.5 us for reading them;
 // 4096 rows of 32 take 3.1 us and one row 3.1 us, a launch's time.  Rows of nothing
