@@ -8,9 +8,9 @@ missing or the device is not sm_100, the calls raise.
 
 Every call runs on the device's current stream, or on the one that ``stream`` (a
 ``torch.cuda.Stream`` or a handle) names.  The arguments of a call on another
-stream must be ready there, and stay as they are until it has run; what it
-allocates belongs to that stream, which the current one waits for before it uses
-an output.
+stream must be ready there, and stay as they are until it has run.  What it
+allocates belongs to that stream: the caller lets the current stream wait for it
+before an output is used there.
 
 Names and semantics match the C entry points:
 
